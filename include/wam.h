@@ -388,6 +388,105 @@ wam_status wam_op_norm_mod(int dtype, const float* dev_x, void* dev_h, int M, in
 wam_status wam_op_attention_noalloc(const void* dev_q, const void* dev_k, const void* dev_v, void* dev_out, int B,
                                     int H, int Lq, int Lk, int Lcache, int splits, void* stream);
 
+/* ---- feed-forward and residual-norm operators, both directions --------- */
+
+/* What the entry points below share.
+ *   - Types: dtype WAM_BF16 (bf16 matrices, products on the tensor cores, fp32
+ *     accumulation) or WAM_FP32 (fp32 everywhere).  Every sum, statistic and
+ *     activation is fp32; an output is rounded once.  Biases, gains,
+ *     modulation vectors and their gradients are fp32.
+ *   - Matrices are row-major and contiguous, aligned to their element; any
+ *     M >= 0 and any sizes from 1 up.  16-byte-aligned pointers and row
+ *     lengths that are multiples of 8 are fastest.  M == 0: outputs with rows
+ *     are empty, gradients that sum over rows are set to zero.
+ *   - Outputs lie apart from each other and from the inputs, unless stated
+ *     (else WAM_ERR_INVALID_ARG).  Bytes outside the outputs are not written.
+ *   - Pointers belong to the current device, and the call enqueues on `stream`
+ *     and returns; it allocates nothing, keeps nothing between calls and can
+ *     be captured.  Calls on several streams or threads may overlap.
+ *   - A backward call takes a workspace of at least the bytes that its
+ *     _workspace call reports (a host computation; 256-byte aligned; NULL when
+ *     it reports 0), which holds intermediates from the call's first kernel
+ *     to its last: calls, or captured graphs, that may run at the same time
+ *     need one each.
+ *   - The same inputs give the same bits (no atomics).
+ *   - A device-side bounded wait that gave up (which a finished kernel never
+ *     sees) is reported, once, by wam_ops_check_status. */
+
+/* Activations. */
+typedef enum {
+  WAM_ACT_NONE = 0,
+  WAM_ACT_RELU = 1,
+  WAM_ACT_SILU = 2,
+  WAM_ACT_GELU_TANH = 3,
+  WAM_ACT_GELU_ERF = 4,
+  WAM_ACT_SIGMOID = 5
+} wam_act;
+
+/* Synchronise the current device; WAM_ERR_TIMEOUT if a bounded wait of one of
+ * these operators gave up on it since the last call (its output is then
+ * incomplete). */
+wam_status wam_ops_check_status(void);
+
+/* y = act(z) + residual, z = x w^T + bias.  x [M, K], w [N, K] of dtype;
+ * bias [N] or NULL; residual [M, N] of out_dtype or NULL, may be y itself
+ * (the residual stream updated in place); y [M, N] of out_dtype (WAM_FP32 or
+ * dtype); z [M, N] of dtype, or NULL when no backward pass needs it. */
+wam_status wam_op_linear_act(int dtype, int out_dtype, const void* dev_x, const void* dev_w, const float* dev_bias,
+                             const void* dev_residual, void* dev_y, void* dev_z, int M, int N, int K, int act,
+                             void* stream);
+/* Its gradients from dy [M, N] of dy_dtype (WAM_FP32 or dtype) and the saved z
+ * (not read for WAM_ACT_NONE): dz = dy act'(z), dx = dz w [M, K], dw = dz^T x
+ * [N, K] of dtype, db = column sums of dz [N].  Each output may be NULL (not
+ * all; x is needed for dw, w for dx).  The residual's gradient is dy itself.
+ * On the bf16 path dz is rounded to bf16 before the products (db is not). */
+wam_status wam_op_linear_act_workspace(int dtype, int M, int N, int K, int act, int dy_dtype, size_t* nbytes);
+wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* dev_x, const void* dev_w, const void* dev_z,
+                                      const void* dev_dy, void* dev_dx, void* dev_dw, float* dev_db, int M, int N,
+                                      int K, int act, void* dev_workspace, size_t nbytes, void* stream);
+
+/* Gated feed-forward: a = act(g) u, g = x wg^T + bias_g, u = x wu^T + bias_u,
+ * both products, the activation and the product of the two in one kernel.
+ * x [M, K], wg / wu [F, K], a [M, F] of dtype; biases [F] or NULL; g and u
+ * [M, F]: both (saved for the backward pass) or neither. */
+wam_status wam_op_gated(int dtype, const void* dev_x, const void* dev_wg, const void* dev_wu, const float* dev_bias_g,
+                        const float* dev_bias_u, void* dev_a, void* dev_g, void* dev_u, int M, int F, int K, int act,
+                        void* stream);
+/* Its gradients from da [M, F] and the saved g, u: dg = da u act'(g), du = da
+ * act(g); dx = dg wg + du wu [M, K]; dwg = dg^T x, dwu = du^T x [F, K]; the
+ * biases' gradients are the column sums of dg and du [F].  dx, the pair of
+ * weight gradients and the pair of bias gradients may each be NULL (not all). */
+wam_status wam_op_gated_workspace(int dtype, int M, int F, int K, size_t* nbytes);
+wam_status wam_op_gated_backward(int dtype, const void* dev_x, const void* dev_wg, const void* dev_wu,
+                                 const void* dev_g, const void* dev_u, const void* dev_da, void* dev_dx, void* dev_dwg,
+                                 void* dev_dwu, float* dev_dbias_g, float* dev_dbias_u, int M, int F, int K, int act,
+                                 void* dev_workspace, size_t nbytes, void* stream);
+
+/* The norms around a block's end, fused with its gate and residual:
+ *   p = post_norm ? post_gain rms(y) : y,  s = alpha x + gate p,
+ *   h = rms(s) gain (1 + scale) + shift,  rms(v) = v / sqrt(mean(v^2) + 1e-6).
+ * x, s [M, D] of res_dtype (WAM_FP32 or dtype), y, h [M, D] of dtype; s may be
+ * x itself and h may be y itself.  post_gain, gain [D] or NULL (1); gate,
+ * scale, shift: one vector [D] per rows_per_group consecutive rows (a sample;
+ * 0: one for all; the last group may be short), group g's at + g ld_mod
+ * floats, or NULL (1, 0, 0).  D <= 8192. */
+wam_status wam_op_residual_norm(int dtype, int res_dtype, const void* dev_x, const void* dev_y, void* dev_s,
+                                void* dev_h, int M, int D, float alpha, int post_norm, const float* dev_post_gain,
+                                const float* dev_gate, const float* dev_gain, const float* dev_scale,
+                                const float* dev_shift, int rows_per_group, int ld_mod, void* stream);
+/* Its gradients from ds [M, D] of res_dtype (NULL: zero) and dh [M, D] of
+ * dtype, at the forward's s and y: dx (may be ds or s itself), dy (may be dh
+ * or y itself), and, each NULL if not wanted, dpost_gain, dgain [D] and dgate,
+ * dscale, dshift [groups, D] (contiguous). */
+wam_status wam_op_residual_norm_workspace(int M, int D, int rows_per_group, size_t* nbytes);
+wam_status wam_op_residual_norm_backward(int dtype, int res_dtype, const void* dev_s, const void* dev_y,
+                                         const void* dev_ds, const void* dev_dh, void* dev_dx, void* dev_dy, int M,
+                                         int D, float alpha, int post_norm, const float* dev_post_gain,
+                                         const float* dev_gate, const float* dev_gain, const float* dev_scale,
+                                         int rows_per_group, int ld_mod, float* dev_dpost_gain, float* dev_dgate,
+                                         float* dev_dgain, float* dev_dscale, float* dev_dshift, void* dev_workspace,
+                                         size_t nbytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ calling anything that needs the library raises if it is missing -- there is
 no CPU fallback.
 """
 from ._binding import (  # noqa: F401
+    ACTS,
     BF16,
     CEWP,
     FP32,
@@ -23,6 +24,16 @@ from ._binding import (  # noqa: F401
     op_attention_noalloc,
     op_linear,
     op_linear_tiled,
+    op_linear_act,
+    op_linear_act_backward,
+    op_linear_act_workspace,
+    op_gated,
+    op_gated_backward,
+    op_gated_workspace,
+    op_residual_norm,
+    op_residual_norm_backward,
+    op_residual_norm_workspace,
+    ops_check_status,
     op_attention_joint,
     op_norm_mod,
     patchify,

@@ -7,6 +7,7 @@ import os
 import numpy as np
 
 FP32, BF16 = 0, 1
+ACTS = ("none", "relu", "silu", "gelu_tanh", "gelu_erf", "sigmoid")  # indexed by wam_act
 SEQUENTIAL, CEWP = 0, 1
 PROF_CLASSES = ("video_norm", "video_qkv", "video_attn", "video_oproj", "video_ffn_up", "video_ffn_down",
                 "video_temb", "video_io", "action_norm", "action_qkv", "action_attn", "action_oproj",
@@ -89,6 +90,18 @@ def lib():
                                             C.c_int, _P]),
         "wam_op_attention": (C.c_int, [C.c_int, _P, _P, _P, _P] + [C.c_int] * 7 + [_P]),
         "wam_op_attention_noalloc": (C.c_int, [_P, _P, _P, _P] + [C.c_int] * 6 + [_P]),
+        "wam_ops_check_status": (C.c_int, []),
+        "wam_op_linear_act": (C.c_int, [C.c_int] * 2 + [_P] * 6 + [C.c_int] * 4 + [_P]),
+        "wam_op_linear_act_workspace": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_size_t)]),
+        "wam_op_linear_act_backward": (C.c_int, [C.c_int] * 2 + [_P] * 7 + [C.c_int] * 4 + [_P, C.c_size_t, _P]),
+        "wam_op_gated": (C.c_int, [C.c_int] + [_P] * 8 + [C.c_int] * 4 + [_P]),
+        "wam_op_gated_workspace": (C.c_int, [C.c_int] * 4 + [C.POINTER(C.c_size_t)]),
+        "wam_op_gated_backward": (C.c_int, [C.c_int] + [_P] * 11 + [C.c_int] * 4 + [_P, C.c_size_t, _P]),
+        "wam_op_residual_norm": (C.c_int, [C.c_int] * 2 + [_P] * 4 + [C.c_int] * 2 + [C.c_float, C.c_int] + [_P] * 5
+                                 + [C.c_int] * 2 + [_P]),
+        "wam_op_residual_norm_workspace": (C.c_int, [C.c_int] * 3 + [C.POINTER(C.c_size_t)]),
+        "wam_op_residual_norm_backward": (C.c_int, [C.c_int] * 2 + [_P] * 6 + [C.c_int] * 2 + [C.c_float, C.c_int]
+                                          + [_P] * 4 + [C.c_int] * 2 + [_P] * 6 + [C.c_size_t, _P]),
         "wam_op_norm_mod": (C.c_int, [C.c_int, _P, _P, C.c_int, C.c_int, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
@@ -364,3 +377,161 @@ def op_attention_noalloc(q, k, v, out, B, H, Lq, Lk, Lcache, splits, stream=None
                                         _stream(stream))
     if st:
         raise WamError(st, "wam_op_attention_noalloc")
+
+
+# ------------------------------- feed-forward and residual-norm operators ---
+_TORCH_TYPES = {FP32: "torch.float32", BF16: "torch.bfloat16"}
+
+
+class _Args:
+    """Pointers of one operator call's device buffers, each checked against
+    what the C ABI assumes of it: a C-contiguous CUDA tensor of the given type
+    and element count, on the current device.  None and raw integer addresses
+    pass through unchecked."""
+
+    def __init__(self, where: str):
+        self.where = where
+        self.device = None
+
+    def __call__(self, name: str, x, dtype: int, n: int, rows=None):
+        """rows: (count, width, stride) of a table whose rows lie `stride` apart."""
+        if x is None or isinstance(x, int):
+            return x
+        if self.device is None:
+            import torch
+            self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        if rows is None or rows[2] == rows[1] or rows[0] == 1:
+            shape_ok = x.is_contiguous() and x.numel() == n
+        else:
+            shape_ok = x.dim() == 2 and tuple(x.shape) == rows[:2] and x.stride() == (rows[2], 1)
+        if not shape_ok and rows is not None and rows[0] == 1:  # one vector of a wider table
+            shape_ok = x.numel() == n and x.stride(-1) == 1
+        if not (shape_ok and x.is_cuda and x.device.index == self.device and str(x.dtype) == _TORCH_TYPES.get(dtype)):
+            want = f"{n} elements" if rows is None else f"{rows[0]} rows of {rows[1]}, {rows[2]} apart"
+            raise WamError(1, self.where, f"{name}: need a contiguous {_TORCH_TYPES.get(dtype)} tensor on the current "
+                           f"device, {want}; got {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
+        return x.data_ptr()
+
+    def workspace(self, x, need: int):
+        """(pointer, bytes) of a workspace tensor of any type (an integer
+        address is taken to hold what the call needs)."""
+        if x is None:
+            return None, 0
+        if isinstance(x, int):
+            return x, need
+        if not (x.is_cuda and x.is_contiguous()):
+            raise WamError(1, self.where, "workspace: need a contiguous CUDA tensor")
+        return x.data_ptr(), x.numel() * x.element_size()
+
+
+def _done(st: int, where: str):
+    if st:
+        raise WamError(st, where)
+
+
+def ops_check_status():
+    """Synchronise; raises if a bounded device wait of an operator below gave up."""
+    _done(lib().wam_ops_check_status(), "wam_ops_check_status")
+
+
+def op_linear_act(dtype, x, w, bias, y, M, N, K, act=0, residual=None, z=None, out_dtype=None, stream=None):
+    """y = act(z) + residual, z = x w^T + bias (wam_op_linear_act).  act: an index
+    of ACTS; residual may be y; z: where to save the pre-activation, or None."""
+    where, out = "wam_op_linear_act", dtype if out_dtype is None else out_dtype
+    a = _Args(where)
+    _done(lib().wam_op_linear_act(dtype, out, a("x", x, dtype, M * K), a("w", w, dtype, N * K), a("bias", bias, FP32, N),
+                                  a("residual", residual, out, M * N), a("y", y, out, M * N), a("z", z, dtype, M * N),
+                                  M, N, K, act, _stream(stream)), where)
+
+
+def op_linear_act_workspace(dtype, M, N, K, act=0, dy_dtype=None) -> int:
+    """Workspace bytes of op_linear_act_backward."""
+    n = C.c_size_t(0)
+    _done(lib().wam_op_linear_act_workspace(dtype, M, N, K, act, dtype if dy_dtype is None else dy_dtype, C.byref(n)),
+          "wam_op_linear_act_workspace")
+    return n.value
+
+
+def op_linear_act_backward(dtype, x, w, z, dy, dx, dw, db, M, N, K, act=0, dy_dtype=None, workspace=None, stream=None):
+    """Gradients of op_linear_act (each of dx, dw, db may be None)."""
+    where, o = "wam_op_linear_act_backward", dtype if dy_dtype is None else dy_dtype
+    a = _Args(where)
+    ws, n = a.workspace(workspace, 1 << 62)
+    _done(lib().wam_op_linear_act_backward(dtype, o, a("x", x, dtype, M * K), a("w", w, dtype, N * K),
+                                           a("z", z, dtype, M * N), a("dy", dy, o, M * N), a("dx", dx, dtype, M * K),
+                                           a("dw", dw, dtype, N * K), a("db", db, FP32, N), M, N, K, act, ws, n,
+                                           _stream(stream)), where)
+
+
+def op_gated(dtype, x, wg, wu, a, M, F, K, act=ACTS.index("silu"), bias_g=None, bias_u=None, g=None, u=None, stream=None):
+    """a = act(x wg^T + bias_g) (x wu^T + bias_u) (wam_op_gated); g and u: where
+    to save the two pre-activations, or None."""
+    where = "wam_op_gated"
+    c = _Args(where)
+    _done(lib().wam_op_gated(dtype, c("x", x, dtype, M * K), c("wg", wg, dtype, F * K), c("wu", wu, dtype, F * K),
+                             c("bias_g", bias_g, FP32, F), c("bias_u", bias_u, FP32, F), c("a", a, dtype, M * F),
+                             c("g", g, dtype, M * F), c("u", u, dtype, M * F), M, F, K, act, _stream(stream)), where)
+
+
+def op_gated_workspace(dtype, M, F, K) -> int:
+    """Workspace bytes of op_gated_backward."""
+    n = C.c_size_t(0)
+    _done(lib().wam_op_gated_workspace(dtype, M, F, K, C.byref(n)), "wam_op_gated_workspace")
+    return n.value
+
+
+def op_gated_backward(dtype, x, wg, wu, g, u, da, dx, dwg, dwu, M, F, K, act=ACTS.index("silu"), dbias_g=None,
+                      dbias_u=None, workspace=None, stream=None):
+    """Gradients of op_gated (dx, the weights' pair and the biases' pair may each be None)."""
+    where = "wam_op_gated_backward"
+    c = _Args(where)
+    ws, n = c.workspace(workspace, 1 << 62)
+    _done(lib().wam_op_gated_backward(dtype, c("x", x, dtype, M * K), c("wg", wg, dtype, F * K), c("wu", wu, dtype, F * K),
+                                      c("g", g, dtype, M * F), c("u", u, dtype, M * F), c("da", da, dtype, M * F),
+                                      c("dx", dx, dtype, M * K), c("dwg", dwg, dtype, F * K), c("dwu", dwu, dtype, F * K),
+                                      c("dbias_g", dbias_g, FP32, F), c("dbias_u", dbias_u, FP32, F), M, F, K, act, ws, n,
+                                      _stream(stream)), where)
+
+
+def _groups(M, rows_per_group):
+    return -(-M // rows_per_group) if rows_per_group else 1
+
+
+def op_residual_norm(dtype, x, y, s, h, M, D, post_norm=False, post_gain=None, gate=None, gain=None, scale=None,
+                     shift=None, alpha=1.0, rows_per_group=0, ld_mod=0, res_dtype=FP32, stream=None):
+    """s = alpha x + gate p, p = y or post_gain rms(y); h = rms(s) gain (1 + scale)
+    + shift (wam_op_residual_norm).  s may be x, h may be y."""
+    where, ld = "wam_op_residual_norm", ld_mod or D
+    c, rows = _Args(where), (_groups(M, rows_per_group), D, ld)
+    n = rows[0] * D
+    _done(lib().wam_op_residual_norm(dtype, res_dtype, c("x", x, res_dtype, M * D), c("y", y, dtype, M * D),
+                                     c("s", s, res_dtype, M * D), c("h", h, dtype, M * D), M, D, alpha, int(post_norm),
+                                     c("post_gain", post_gain, FP32, D), c("gate", gate, FP32, n, rows),
+                                     c("gain", gain, FP32, D), c("scale", scale, FP32, n, rows),
+                                     c("shift", shift, FP32, n, rows), rows_per_group, ld, _stream(stream)), where)
+
+
+def op_residual_norm_workspace(M, D, rows_per_group=0) -> int:
+    """Workspace bytes of op_residual_norm_backward."""
+    n = C.c_size_t(0)
+    _done(lib().wam_op_residual_norm_workspace(M, D, rows_per_group, C.byref(n)), "wam_op_residual_norm_workspace")
+    return n.value
+
+
+def op_residual_norm_backward(dtype, s, y, ds, dh, dx, dy, M, D, post_norm=False, post_gain=None, gate=None, gain=None,
+                              scale=None, alpha=1.0, rows_per_group=0, ld_mod=0, res_dtype=FP32, dpost_gain=None,
+                              dgate=None, dgain=None, dscale=None, dshift=None, workspace=None, stream=None):
+    """Gradients of op_residual_norm at its output s and its input y; ds may be
+    None (zero), every parameter gradient too (not computed).  dx may be ds or
+    s, dy may be dh or y."""
+    where, ld = "wam_op_residual_norm_backward", ld_mod or D
+    c, rows = _Args(where), (_groups(M, rows_per_group), D, ld)
+    n = rows[0] * D
+    ws, nb = c.workspace(workspace, 1 << 62)
+    _done(lib().wam_op_residual_norm_backward(
+        dtype, res_dtype, c("s", s, res_dtype, M * D), c("y", y, dtype, M * D), c("ds", ds, res_dtype, M * D),
+        c("dh", dh, dtype, M * D), c("dx", dx, res_dtype, M * D), c("dy", dy, dtype, M * D), M, D, alpha, int(post_norm),
+        c("post_gain", post_gain, FP32, D), c("gate", gate, FP32, n, rows), c("gain", gain, FP32, D),
+        c("scale", scale, FP32, n, rows), rows_per_group, ld, c("dpost_gain", dpost_gain, FP32, D),
+        c("dgate", dgate, FP32, n), c("dgain", dgain, FP32, D), c("dscale", dscale, FP32, n),
+        c("dshift", dshift, FP32, n), ws, nb, _stream(stream)), where)

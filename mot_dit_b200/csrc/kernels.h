@@ -383,6 +383,118 @@ cudaError_t launch_tacd_targets(const float* a_t, const float* a0_teacher, const
                                 const float* f_ema, float t, float lambda, int B, int per_sample, float* u_ta,
                                 float* v_student, float* u_cd, float* losses, cudaStream_t s);
 
+// ---- feed-forward products, both directions (gemm_ops.cu, ffn_ops.cu) ------
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGeluTanh = 3, kActGeluErf = 4, kActSigmoid = 5, kActKinds = 6 };
+
+// Epilogue of one product: out = act(acc + bias) + res (res: out's type, may
+// be out itself), z = acc + bias in the operands' type; gated: out = act(g +
+// bias) (u + bias2), z / z2 = the two pre-activations.  All matrices have
+// rows ld apart.  vec: every pointer 16-byte aligned and ld a multiple of 8.
+struct OpEpi {
+  void* out;
+  const float* bias;
+  const float* bias2;
+  const void* res;
+  void* z;
+  void* z2;
+  int ld;
+  int act;
+  int out_f32;
+  int vec;
+};
+
+// A stored matrix: `outer` rows of `inner` contiguous elements, rows ld apart.
+struct OpMat {
+  const void* p;
+  int ld, inner, outer;
+};
+
+// C[m, n] = sum over up to two operand pairs i of sum_k A_i[m, k] B_i[n, k].
+// a_mn / b_mn: the operand is stored with its reduction index outermost
+// ([K][M] / [K][N]; the pass that needs it never transposes it in memory).
+// gated: one A, two B of N rows each; C has the columns of both (g, u).
+// Every A_i (B_i) of a product has the same shape.
+struct OpProduct {
+  OpMat a[2], b[2];
+  int pairs;  // 1 or 2 (2: gated is 0)
+  int M, N, K;
+  int a_mn, b_mn, gated;
+  OpEpi e;
+};
+
+// Column sums of partial rows, out[c] = sum_r part[r][c], added by the
+// product's otherwise idle warps (nullptr: none).
+struct OpColSum {
+  const float* part;
+  float* out;
+  int rows, cols;
+};
+
+constexpr int kOpProducts = 3;
+// All products of the list in one launch (bf16 operands, fp32 accumulators).
+cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s);
+// The same in fp32 on the CUDA cores.
+cudaError_t launch_op_gemm_f32(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s);
+
+// dz = dy act'(z) (z null: dz = dy) as the compute type, rows ld_dz apart (dz
+// null: sums only), and per row chunk the column sums of dz before rounding,
+// part[chunk][N] (null: none).  Gated: dg = da u act'(g), du = da act(g), the
+// sums of du behind those of dg ([2][chunks][N]).
+struct ActGrad {
+  const void* dy;   // [M, N], fp32 if dy_f32
+  const void* z;    // [M, N] compute type (gated: g)
+  const void* u;    // gated
+  void* dz;         // gated: dg
+  void* du;
+  float* part;
+  int M, N, ld_dz, act, f32, dy_f32, chunks;
+};
+int act_grad_chunks(int M);
+// The sums alone (a call that wants no product).
+cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s);
+cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);
+// dst[r][c] = src[r][c] (bf16), src rows `cols` apart, dst rows ld apart.
+cudaError_t launch_repack(const void* src, void* dst, int rows, int cols, int ld, cudaStream_t s);
+
+// s = alpha x + gate p, p = y or post_gain rms(y); h = rms(s) gain (1 +
+// scale) + shift.  Stream types: x / s fp32 if res_f32 else bf16; y / h fp32
+// if f32 else bf16.  gate / scale / shift: rows ld_mod apart, one per
+// rows_per_group rows (any may be null).
+struct ResNorm {
+  const void* x;
+  const void* y;
+  void* s;
+  void* h;
+  const float* post_gain;
+  const float* gate;
+  const float* gain;
+  const float* scale;
+  const float* shift;
+  float alpha;
+  int M, D, post, rows_per_group, ld_mod, f32, res_f32;
+};
+constexpr int kResNormMax = 8192;  // widest row
+cudaError_t launch_res_norm(const ResNorm& a, cudaStream_t s);
+// Backward at the stored stream s (a.x) and y: dx, dy and the parameter
+// gradients (each may be null); part: res_norm_part_floats floats.
+struct ResNormGrad {
+  ResNorm f;        // x = the forward's s; s / h unused
+  const void* ds;   // [M, D] stream type, null: zero
+  const void* dh;   // [M, D] compute type
+  void* dx;
+  void* dy;
+  float* dpost_gain;
+  float* dgate;
+  float* dgain;
+  float* dscale;
+  float* dshift;
+  float* part;
+};
+size_t res_norm_part_floats(int M, int D, int rows_per_group);
+cudaError_t launch_res_norm_grad(const ResNormGrad& a, cudaStream_t s);
+// Bits of the bounded waits that gave up on the current device, and clears them (synchronous).
+cudaError_t op_gemm_status(unsigned* bits);
+
 // TMA tensor-map creation (driver entry point resolved at run time).
 bool make_tmap_3d(CUtensorMap* map, const void* base, int K, int rows, int nmat, size_t mat_stride_bytes,
                   int box_rows);
@@ -390,5 +502,8 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, int K, int rows, int nmat,
 // dims (inner, rows, nmat), box (box_inner, box_rows, 1).
 bool make_tmap_sw128(CUtensorMap* map, const void* base, int elem_bytes, int inner, int rows, int nmat,
                      size_t mat_stride_bytes, int box_inner, int box_rows);
+// bf16 matrix of `rows` rows of `inner` elements, rows ld elements apart (a
+// multiple of 8), box 64 x box_rows, 128-byte swizzle.
+bool make_tmap_rows(CUtensorMap* map, const void* base, int inner, int rows, int ld, int box_rows);
 
 }  // namespace wam

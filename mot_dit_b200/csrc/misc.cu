@@ -446,4 +446,17 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, int K, int rows, int nmat,
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_rows(CUtensorMap* map, const void* base, int inner, int rows, int ld, int box_rows) {
+  if (!encoder_ready()) return false;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) || ld % 8) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2};  // (one matrix: the outer stride is unused)
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace wam

@@ -1,0 +1,324 @@
+"""The feed-forward and residual-norm operators on the GPU against their
+64-bit definitions, elementwise, with bounds from the arithmetic (ffn_testlib)."""
+import pytest
+
+import mot_dit_b200 as W
+
+torch = pytest.importorskip("torch")
+import ffn_testlib as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float32
+CODE = {BF: W.BF16, FP: W.FP32}
+ACT = {n: i for i, n in enumerate(W.ACTS)}
+
+
+def _ws(nbytes):
+    return torch.full((max(nbytes, 1),), 255, dtype=torch.uint8, device="cuda") if nbytes else None  # (NaN patterns)
+
+
+@pytest.fixture(autouse=True)
+def _no_timeout():
+    yield
+    W.ops_check_status()
+
+
+# rows: one token, a few, ragged tiles, several row tiles; features and
+# reductions that no tile or vector divides; long reductions with few tiles
+# (cluster split), many tiles (CTA pairs).
+LINEAR = [
+    # M, N, K, act, type, out, residual, save z
+    (1, 1, 1, "none", BF, BF, False, False),
+    (1, 64, 64, "silu", BF, FP, True, True),
+    (1, 1000, 1536, "gelu_tanh", BF, BF, False, False),
+    (3, 77, 130, "gelu_erf", BF, BF, True, True),
+    (16, 384, 6144, "none", BF, FP, True, False),
+    (17, 40, 72, "relu", BF, BF, True, True),
+    (129, 200, 328, "sigmoid", BF, FP, True, True),
+    (130, 4111, 200, "gelu_tanh", BF, BF, True, True),
+    (200, 264, 511, "silu", BF, BF, False, True),
+    (1088, 1536, 768, "none", BF, FP, True, False),
+    (2100, 2049, 136, "gelu_tanh", BF, BF, True, False),
+    (2560, 2560, 256, "silu", BF, BF, False, True),
+    (1, 33, 65, "gelu_tanh", FP, FP, True, True),
+    (70, 129, 1030, "silu", FP, FP, True, False),
+    (260, 516, 96, "gelu_erf", FP, FP, False, True),
+    (1500, 2000, 70, "relu", FP, FP, True, True),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act,t,o,res,save", LINEAR)
+def test_linear(M, N, K, act, t, o, res, save):
+    n = T.normals(M + N + K)
+    x, w, b = n(M, K, dtype=t), n(N, K, std=K ** -0.5, dtype=t), n(N, std=0.3)
+    r = n(M, N, dtype=o) if res else None
+    (y, oky), (z, okz) = T.guarded((M, N), o), T.guarded((M, N), t)
+    W.op_linear_act(CODE[t], x, w, b, y, M, N, K, act=ACT[act], residual=r, z=z if save else None, out_dtype=CODE[o])
+    z64, ez, y64, ey = T.linear64(x, w, b, r, act, o)
+    T.within(y, y64, ey)
+    oky()
+    if save:
+        T.within(z, z64, ez)
+        okz()
+    y2 = torch.empty_like(y)
+    W.op_linear_act(CODE[t], x, w, b, y2, M, N, K, act=ACT[act], residual=r, out_dtype=CODE[o])
+    assert torch.equal(y, y2)  # the same bits, with or without z
+    if res:  # in place on the residual
+        W.op_linear_act(CODE[t], x, w, b, r, M, N, K, act=ACT[act], residual=r, out_dtype=CODE[o])
+        assert torch.equal(r, y2)
+
+
+@pytest.mark.parametrize("t", [BF, FP])
+@pytest.mark.parametrize("sx,sw,sy", [(1, 0, 0), (0, 3, 0), (0, 0, 1), (1, 1, 1)])
+def test_linear_unaligned(t, sx, sw, sy):
+    """Operands and outputs that start off a 16-byte boundary."""
+    M, N, K = 150, 136, 200
+    n = T.normals(sx * 100 + sw * 10 + sy)
+    put = lambda v, s: torch.cat([torch.zeros(s, dtype=v.dtype, device="cuda"), v.flatten()])[s:].view(v.shape)  # noqa: E731
+    x, w = put(n(M, K, dtype=t), sx), put(n(N, K, std=K ** -0.5, dtype=t), sw)
+    b, r = put(n(N), sy), put(n(M, N, dtype=t), sy)
+    (y, oky), (z, okz) = T.guarded((M, N), t, sy), T.guarded((M, N), t, sy)
+    W.op_linear_act(CODE[t], x, w, b, y, M, N, K, act=ACT["silu"], residual=r, z=z)
+    z64, ez, y64, ey = T.linear64(x, w, b, r, "silu", t)
+    T.within(y, y64, ey)
+    T.within(z, z64, ez)
+    oky(), okz()
+
+
+LINEAR_BWD = [
+    (1, 1, 1, "silu", BF, BF),
+    (1, 65, 64, "none", BF, BF),
+    (33, 64, 64, "none", BF, BF),
+    (33, 64, 64, "none", BF, FP),
+    (100, 71, 200, "gelu_tanh", BF, FP),
+    (257, 4111, 264, "gelu_tanh", BF, BF),
+    (1000, 129, 67, "gelu_erf", BF, BF),
+    (8448, 64, 72, "silu", BF, BF),
+    (64, 72, 3000, "sigmoid", BF, FP),
+    (2049, 1544, 1100, "relu", BF, BF),
+    (40, 33, 65, "silu", FP, FP),
+    (2048, 36, 40, "none", FP, FP),
+    (300, 777, 321, "gelu_tanh", FP, FP),
+]
+
+
+@pytest.mark.parametrize("M,N,K,act,t,o", LINEAR_BWD)
+def test_linear_backward(M, N, K, act, t, o):
+    n = T.normals(M + 3 * N + K)
+    x, w, dy = n(M, K, dtype=t), n(N, K, std=K ** -0.5, dtype=t), n(M, N, dtype=o)
+    z = n(M, N, dtype=t, std=1.5) if act != "none" else None
+    (dx, ok1), (dw, ok2), (db, ok3) = T.guarded((M, K), t), T.guarded((N, K), t), T.guarded((N,), FP)
+    need = W.op_linear_act_workspace(CODE[t], M, N, K, act=ACT[act], dy_dtype=CODE[o])
+    call = lambda a, b, c: W.op_linear_act_backward(CODE[t], x, w, z, dy, a, b, c, M, N, K, act=ACT[act],  # noqa: E731
+                                                    dy_dtype=CODE[o], workspace=_ws(need))
+    call(dx, dw, db)
+    (dx64, ex), [((dw64, ew), (db64, eb))] = T.linear_grad64(x, w, z, dy, act)
+    T.within(dx, dx64, ex)
+    T.within(dw, dw64, ew)
+    T.within(db, db64, eb)
+    ok1(), ok2(), ok3()
+    # each gradient alone, within the same bounds
+    a, b, c = torch.empty_like(dx), torch.empty_like(dw), torch.empty_like(db)
+    call(a, None, None), call(None, b, None), call(None, None, c)
+    T.within(a, dx64, ex), T.within(b, dw64, ew)
+    assert torch.equal(c, db)
+
+
+GATED = [
+    (1, 1, 1, "silu", BF, True, True),
+    (1, 64, 64, "silu", BF, False, False),
+    (1, 1000, 1536, "gelu_tanh", BF, True, False),
+    (5, 33, 71, "sigmoid", BF, True, True),
+    (140, 100, 200, "relu", BF, False, True),
+    (129, 777, 136, "gelu_erf", BF, True, True),
+    (1088, 1536, 256, "silu", BF, True, True),
+    (2600, 2200, 128, "gelu_tanh", BF, False, False),
+    (64, 40, 4096, "silu", BF, True, True),
+    (150, 130, 201, "none", BF, True, True),
+    (3, 20, 33, "silu", FP, True, True),
+    (130, 300, 200, "gelu_erf", FP, False, True),
+    (1000, 1100, 60, "gelu_tanh", FP, True, False),
+]
+
+
+@pytest.mark.parametrize("M,F,K,act,t,bias,save", GATED)
+def test_gated(M, F, K, act, t, bias, save):
+    n = T.normals(M + F + K)
+    x, wg, wu = n(M, K, dtype=t), n(F, K, std=K ** -0.5, dtype=t), n(F, K, std=K ** -0.5, dtype=t)
+    bg, bu = (n(F, std=0.3), n(F, std=0.3)) if bias else (None, None)
+    (a, ok1), (g, ok2), (u, ok3) = (T.guarded((M, F), t) for _ in range(3))
+    kw = dict(act=ACT[act], bias_g=bg, bias_u=bu)
+    W.op_gated(CODE[t], x, wg, wu, a, M, F, K, g=g if save else None, u=u if save else None, **kw)
+    (a64, ea), (g64, eg), (u64, eu) = T.gated64(x, wg, wu, bg, bu, act)
+    T.within(a, a64, ea)
+    ok1()
+    if save:
+        T.within(g, g64, eg), T.within(u, u64, eu)
+        ok2(), ok3()
+    a2 = torch.empty_like(a)
+    W.op_gated(CODE[t], x, wg, wu, a2, M, F, K, **kw)
+    assert torch.equal(a, a2)
+
+
+GATED_BWD = [
+    (1, 1, 1, "silu", BF, True),
+    (33, 64, 64, "silu", BF, True),
+    (100, 71, 200, "gelu_tanh", BF, False),
+    (300, 333, 67, "gelu_erf", BF, True),
+    (2112, 1024, 768, "silu", BF, True),
+    (8448, 40, 64, "sigmoid", BF, True),
+    (50, 2000, 72, "relu", BF, True),
+    (264, 777, 321, "silu", FP, True),
+    (20, 33, 65, "gelu_tanh", FP, False),
+]
+
+
+@pytest.mark.parametrize("M,F,K,act,t,bias", GATED_BWD)
+def test_gated_backward(M, F, K, act, t, bias):
+    n = T.normals(M + 3 * F + K)
+    x, wg, wu = n(M, K, dtype=t), n(F, K, std=K ** -0.5, dtype=t), n(F, K, std=K ** -0.5, dtype=t)
+    g, u, da = n(M, F, dtype=t, std=1.5), n(M, F, dtype=t), n(M, F, dtype=t)
+    outs = [T.guarded(s, d) for s, d in (((M, K), t), ((F, K), t), ((F, K), t), ((F,), FP), ((F,), FP))]
+    dx, dwg, dwu, dbg, dbu = (o[0] for o in outs)
+    ws = _ws(W.op_gated_workspace(CODE[t], M, F, K))
+    call = lambda a, b, c, d, e: W.op_gated_backward(CODE[t], x, wg, wu, g, u, da, a, b, c, M, F, K, act=ACT[act],  # noqa: E731
+                                                     dbias_g=d, dbias_u=e, workspace=ws)
+    call(dx, dwg, dwu, dbg if bias else None, dbu if bias else None)
+    (dx64, ex), [((g64, eg), (bg64, ebg)), ((u64, eu), (bu64, ebu))] = T.gated_grad64(x, wg, wu, g, u, da, act)
+    T.within(dx, dx64, ex), T.within(dwg, g64, eg), T.within(dwu, u64, eu)
+    if bias:
+        T.within(dbg, bg64, ebg), T.within(dbu, bu64, ebu)
+        c, d = torch.empty_like(dbg), torch.empty_like(dbu)
+        call(None, None, None, c, d)
+        assert torch.equal(c, dbg) and torch.equal(d, dbu)
+    for _, ok in outs:
+        ok()
+    a, b, c = torch.empty_like(dx), torch.empty_like(dwg), torch.empty_like(dwu)
+    call(a, None, None, None, None), call(None, b, c, None, None)
+    T.within(a, dx64, ex), T.within(b, g64, eg), T.within(c, u64, eu)
+
+
+NORM = [
+    # M, per, D, types (stream, compute), post, gate, mod, gain, alpha
+    (1, 0, 1, FP, BF, True, True, True, True, 1.0),
+    (1, 0, 768, FP, BF, True, True, True, True, 1.0),
+    (5, 0, 3, FP, BF, True, False, False, False, 1.0),
+    (37, 10, 33, BF, BF, True, True, True, True, 0.5),
+    (100, 34, 64, FP, BF, False, True, True, False, 1.0),
+    (300, 1, 264, FP, BF, True, True, True, True, 1.0),
+    (700, 100, 1536, FP, BF, True, True, True, False, 1.0),
+    (333, 0, 1537, BF, BF, True, True, True, True, -1.25),
+    (90, 30, 520, BF, BF, False, False, False, False, 1.0),
+    (61, 0, 4096, FP, BF, True, True, False, True, 1.0),
+    (40, 20, 8192, FP, BF, True, True, True, True, 1.0),
+    (23, 8, 5003, BF, BF, True, True, True, True, 1.0),
+    (50, 25, 100, FP, FP, True, True, True, True, 1.0),
+    (65, 0, 2049, FP, FP, False, True, True, True, 1.0),
+]
+
+
+def _norm_case(M, per, D, r, t, post, gate, mod, gain):
+    n = T.normals(M + D)
+    p = per or M
+    G = -(-M // p)
+    table = n(G, 3, D, std=0.5)
+    v = dict(post_gain=n(D, std=0.2, mean=1.0) if post else None, gate=table[:, 0] if gate else None,
+             gain=n(D, std=0.2, mean=1.0) if gain else None, scale=table[:, 1] if mod else None,
+             shift=table[:, 2] if mod else None)
+    return n, p, G, n(M, D, std=2.0, dtype=r), n(M, D, std=0.7, dtype=t), v
+
+
+def _d(v):
+    return {k: None if x is None else x.double() for k, x in v.items()}
+
+
+@pytest.mark.parametrize("M,per,D,r,t,post,gate,mod,gain,alpha", NORM)
+def test_residual_norm(M, per, D, r, t, post, gate, mod, gain, alpha):
+    n, p, G, x, y, v = _norm_case(M, per, D, r, t, post, gate, mod, gain)
+    (s, ok1), (h, ok2) = T.guarded((M, D), r), T.guarded((M, D), t)
+    kw = dict(post_norm=post, alpha=alpha, rows_per_group=per, ld_mod=3 * D, res_dtype=CODE[r], **v)
+    W.op_residual_norm(CODE[t], x, y, s, h, M, D, **kw)
+    s64, h64 = T.norm64(x.double(), y.double(), post, alpha=alpha, per=p, **_d(v))
+    # p carries the statistic's error: D + 8 additions and roundings; s two more
+    rel = (D + 16) * 2.0 ** -24
+    part = (s64 - alpha * x.double()).abs()
+    es = rel * part + 2.0 ** -22 * (s64.abs() + (alpha * x.double()).abs())
+    T.within(s, s64, es + T.H[r] * (s64.abs() + es))
+    # h = s r m + b: r's error is that of the mean of s^2, which the errors of s shift by their own share
+    rms = (s64 * s64).mean(1, keepdim=True).add(T.EPS).sqrt()
+    mul = torch.ones(M, D, device="cuda", dtype=torch.float64)
+    if gain:
+        mul = mul * v["gain"].double()
+    if mod:
+        mul = mul * (1 + T.spread(v["scale"], M, p))
+    shift = es.norm(dim=1, keepdim=True) / (D ** 0.5 * rms)
+    eh = mul.abs() / rms * (es + s64.abs() * (rel + 2 * shift)) + 2.0 ** -21 * (h64.abs() + (s64 / rms * mul).abs())
+    T.within(h, h64, eh + T.H[t] * (h64.abs() + eh))
+    ok1(), ok2()
+    s2, h2 = x.clone(), y.clone()  # in place
+    W.op_residual_norm(CODE[t], s2, h2, s2, h2, M, D, **kw)
+    assert torch.equal(s2, s) and torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("M,per,D,r,t,post,gate,mod,gain,alpha", NORM)
+def test_residual_norm_backward(M, per, D, r, t, post, gate, mod, gain, alpha):
+    n, p, G, s, y, v = _norm_case(M, per, D, r, t, post, gate, mod, gain)
+    dh, ds = n(M, D, dtype=t), n(M, D, dtype=r)
+    outs = {"dx": T.guarded((M, D), r), "dy": T.guarded((M, D), t)}
+    for k, x in v.items():
+        if x is not None:
+            outs["d" + k] = T.guarded(tuple(x.shape), FP)
+    kw = dict(post_norm=post, alpha=alpha, rows_per_group=per, ld_mod=3 * D, res_dtype=CODE[r],
+              **{k: x for k, x in v.items() if k != "shift"})
+    ws = _ws(W.op_residual_norm_workspace(M, D, per))
+    W.op_residual_norm_backward(CODE[t], s, y, ds, dh, outs["dx"][0], outs["dy"][0], M, D, workspace=ws, **kw,
+                                **{k: o[0] for k, o in outs.items() if k not in ("dx", "dy")})
+    # the definition's gradient at the point whose stream value is s
+    vd = {k: None if x is None else x.double().requires_grad_() for k, x in v.items()}
+    yd = y.double().requires_grad_()
+    with torch.no_grad():
+        s0, _ = T.norm64(torch.zeros_like(s).double(), yd, post, alpha=alpha, per=p, **vd)
+    xd = ((s.double() - s0) / alpha).requires_grad_()
+    s64, h64 = T.norm64(xd, yd, post, alpha=alpha, per=p, **vd)
+    names = [k for k in vd if vd[k] is not None]
+    got = torch.autograd.grad([s64, h64], [xd, yd] + [vd[k] for k in names], [ds.double(), dh.double()])
+    want = dict(zip(["dx", "dy"] + ["d" + k for k in names], got))
+    # Error bound: every factor of dv, dy and the column terms carries at most rel; the sums over a row and
+    # the expansion of mean(dp post_gain q) are bounded with absolute values throughout.
+    rel = (D + 32) * 2.0 ** -23
+    one = torch.ones(M, D, device="cuda", dtype=torch.float64)
+    rows = lambda x: one if x is None else T.spread(x, M, p)  # noqa: E731
+    vec = lambda x: one if x is None else one * x.double()  # noqa: E731
+    with torch.no_grad():
+        S, Y, DH, DS = s.double().abs(), y.double().abs(), dh.double().abs(), ds.double().abs()
+        mul = (vec(v["gain"]) * (1 + T.spread(v["scale"], M, p)) if mod else vec(v["gain"])).abs()
+        w = (rows(v["gate"]) * vec(v["post_gain"])).abs()
+        r_ = 1 / ((S * S).mean(1, keepdim=True) + T.EPS).sqrt()
+        ry = 1 / ((Y * Y).mean(1, keepdim=True) + T.EPS).sqrt() if post else one[:, :1]
+        mag = lambda a, b: (a * b).mean(1, keepdim=True)  # noqa: E731
+        c = r_ ** 3 * mag(DH * mul, S)
+        dv = DS + r_ * DH * mul + S * c
+        dy = ry * (dv * w + Y * ry ** 2 * mag(dv * w, Y)) if post else dv * w
+        q = Y * ry
+        cols = {"dx": abs(alpha) * dv, "dy": dy}
+        grp = lambda a: torch.stack([a[i * p:(i + 1) * p].sum(0) for i in range(G)])  # noqa: E731
+        cols["dgate"] = grp(dv * q * vec(v["post_gain"]).abs())
+        cols["dpost_gain"] = (dv * q * rows(v["gate"]).abs()).sum(0)
+        cols["dscale"] = grp(DH * S * r_ * vec(v["gain"]).abs())
+        cols["dshift"] = grp(DH)
+        cols["dgain"] = (DH * S * r_ * ((1 + rows(v["scale"])).abs() if mod else 1)).sum(0)
+    for k, (o, ok) in outs.items():
+        row = k in ("dx", "dy")
+        e = (rel + (0 if row else M * 2.0 ** -24)) * cols[k]
+        T.within(o, want[k].reshape(o.shape), e + T.H[o.dtype] * (want[k].reshape(o.shape).abs() + e))
+        ok()
+    # in place on the gradients, without the parameter gradients: the same bits
+    a, b = ds.clone(), dh.clone()
+    W.op_residual_norm_backward(CODE[t], s, y, a, b, a, b, M, D, **kw)
+    assert torch.equal(a, outs["dx"][0]) and torch.equal(b, outs["dy"][0])
+    # no gradient from the stream
+    a, b, zero = torch.empty_like(ds), torch.empty_like(dh), torch.zeros_like(ds)
+    a2, b2 = torch.empty_like(ds), torch.empty_like(dh)
+    W.op_residual_norm_backward(CODE[t], s, y, None, dh, a, b, M, D, **kw)
+    W.op_residual_norm_backward(CODE[t], s, y, zero, dh, a2, b2, M, D, **kw)
+    assert torch.equal(a, a2) and torch.equal(b, b2)
