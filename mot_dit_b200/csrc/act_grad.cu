@@ -17,14 +17,19 @@ namespace wam {
 namespace {
 
 constexpr int kRows = 8;    // row lanes of a block
-constexpr int kAhead = 4;   // rows a thread has in flight
 
-template <int E, bool GATED, bool F32>
+// T: the compute type, DY: the incoming gradient's.
+template <int E, bool GATED, typename T, typename DY>
 __global__ void __launch_bounds__(32 * kRows) act_grad_kernel(const ActGrad a) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int kAhead = E == 1 ? 8 : 4;  // rows a thread has in flight
   __shared__ float sh[GATED ? 2 : 1][kRows][32 * E];
   const int tx = threadIdx.x, ty = threadIdx.y;
   const int n = (blockIdx.x * 32 + tx) * E, chunk = blockIdx.y;
   const int lo = (int)((long long)a.M * chunk / a.chunks), hi = (int)((long long)a.M * (chunk + 1) / a.chunks);
+  const DY* dy = reinterpret_cast<const DY*>(a.dy);
+  const T* pz = reinterpret_cast<const T*>(a.z);
+  const T* pu = reinterpret_cast<const T*>(a.u);
   pdl_trigger();
   pdl_wait();
   float s0[E], s1[E];
@@ -32,37 +37,42 @@ __global__ void __launch_bounds__(32 * kRows) act_grad_kernel(const ActGrad a) {
   for (int j = 0; j < E; ++j) s0[j] = s1[j] = 0.f;
   if (n < a.N) {
     for (int r0 = lo + ty; r0 < hi; r0 += kRows * kAhead) {
-      float d[kAhead][E], z[kAhead][E], u[kAhead][E];
+      Raw<DY, E> rd[kAhead];
+      Raw<T, E> rz[kAhead], ru[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int r = r0 + i * kRows;
-        if (r >= hi) break;
-        const size_t at = (size_t)r * a.N + n;
-        load_any<E>(a.dy, F32 || a.dy_f32, at, d[i]);
-        if (a.z) load_any<E>(a.z, F32, at, z[i]);
-        if (GATED) load_any<E>(a.u, F32, at, u[i]);
+        if (r < hi) {
+          const size_t at = (size_t)r * a.N + n;
+          rd[i].load(dy + at);
+          if (pz) rz[i].load(pz + at);
+          if (GATED) ru[i].load(pu + at);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int r = r0 + i * kRows;
         if (r >= hi) break;
         const size_t at = (size_t)r * a.ld_dz + n;
-        float o0[E], o1[E];
+        float d[E], z[E], u[E], o0[E], o1[E];
+        rd[i].get(d);
+        if (pz) rz[i].get(z);
+        if (GATED) ru[i].get(u);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           float act = 0.f, der = 1.f;
-          if (a.z) act_and_grad<!F32>(a.act, z[i][j], act, der);
+          if (pz) act_and_grad<!F32>(a.act, z[j], act, der);
           if (GATED) {
-            o0[j] = d[i][j] * u[i][j] * der;
-            o1[j] = d[i][j] * act;
+            o0[j] = d[j] * u[j] * der;
+            o1[j] = d[j] * act;
             s1[j] += o1[j];
           } else {
-            o0[j] = d[i][j] * der;
+            o0[j] = d[j] * der;
           }
           s0[j] += o0[j];
         }
-        if (a.dz) store_any<E>(a.dz, F32, at, o0);
-        if (GATED) store_any<E>(a.du, F32, at, o1);
+        if (a.dz) store_to<E>(reinterpret_cast<T*>(a.dz) + at, o0);
+        if (GATED) store_to<E>(reinterpret_cast<T*>(a.du) + at, o1);
       }
     }
   }
@@ -86,10 +96,15 @@ __global__ void __launch_bounds__(32 * kRows) act_grad_kernel(const ActGrad a) {
   }
 }
 
-template <int E, bool GATED, bool F32>
+template <int E, bool GATED, typename T, typename DY>
 cudaError_t run(const ActGrad& a, cudaStream_t s) {
   const dim3 grid((a.N + 32 * E - 1) / (32 * E), a.chunks);
-  return launch_k(act_grad_kernel<E, GATED, F32>, grid, dim3(32, kRows), 0, s, a);
+  return launch_k(act_grad_kernel<E, GATED, T, DY>, grid, dim3(32, kRows), 0, s, a);
+}
+template <int E, typename T>
+cudaError_t run_types(const ActGrad& a, cudaStream_t s) {
+  if (a.u) return run<E, true, T, T>(a, s);
+  return a.dy_f32 ? run<E, false, T, float>(a, s) : run<E, false, T, T>(a, s);
 }
 
 __global__ void __launch_bounds__(256) repack_kernel(const OpMat src, __nv_bfloat16* __restrict__ dst, int ld) {
@@ -127,15 +142,9 @@ int act_grad_chunks(int M) { return std::max(1, std::min(64, (M + 15) / 16)); }
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const bool ptrs = al(a.dy) && al(a.z) && al(a.u) && al(a.dz) && al(a.du);
-  const bool gated = a.u != nullptr;
-  if (a.f32) {
-    const bool v = ptrs && a.N % 4 == 0 && a.ld_dz % 4 == 0;
-    return gated ? (v ? run<4, true, true>(a, s) : run<1, true, true>(a, s))
-                 : (v ? run<4, false, true>(a, s) : run<1, false, true>(a, s));
-  }
-  const bool v = ptrs && a.N % 8 == 0 && a.ld_dz % 8 == 0;
-  return gated ? (v ? run<8, true, false>(a, s) : run<1, true, false>(a, s))
-               : (v ? run<8, false, false>(a, s) : run<1, false, false>(a, s));
+  if (a.f32)
+    return ptrs && a.N % 4 == 0 && a.ld_dz % 4 == 0 ? run_types<4, float>(a, s) : run_types<1, float>(a, s);
+  return ptrs && a.N % 8 == 0 && a.ld_dz % 8 == 0 ? run_types<8, __nv_bfloat16>(a, s) : run_types<1, __nv_bfloat16>(a, s);
 }
 
 cudaError_t launch_repack(const void* src, void* dst, int rows, int cols, int ld, cudaStream_t s) {

@@ -69,6 +69,7 @@ struct GemmArgs {
   int np, n_sums, tiles;
   int stages, stage_bytes;
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
+  int nbuf, nseg;  // accumulator buffers, and segments of each
   int tm_cols;  // tensor-memory columns to allocate
 };
 
@@ -123,11 +124,10 @@ __device__ __forceinline__ void finish_vec(const OpEpi& e, const uint8_t* stg, i
   for (int h = 0; h < 2; ++h) {
     float r[4][E];
     if (!GATED && e.res) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      load_batch<E, 4>(e.res, e.out_f32, [&](int i) {
         const int m = m0 + (4 * h + i) * 4 + (lane >> 3);
-        if (m < M) load_any<E>(e.res, e.out_f32, (size_t)m * e.ld + n, r[i]);
-      }
+        return m < M ? (long long)m * e.ld + n : -1ll;
+      }, r);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -162,11 +162,9 @@ __device__ __forceinline__ void finish_any(const OpEpi& e, const uint8_t* stg, i
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += 8) {
       float res[8][1];
-      if (!GATED && e.res) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (r0 + i < rows) load_any<1>(e.res, e.out_f32, (size_t)(m0 + r0 + i) * e.ld + n, res[i]);
-      }
+      if (!GATED && e.res)
+        load_batch<1, 8>(e.res, e.out_f32,
+                         [&](int i) { return r0 + i < rows ? (long long)(m0 + r0 + i) * e.ld + n : -1ll; }, res);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = r0 + i;
@@ -242,7 +240,11 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   if (CG == 2) cluster_sync();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int buf_cols = g.tm_cols / 2;
+  // Accumulator buffers, nseg segments each: a segment takes up to seg_blocks
+  // k-blocks, and the epilogue adds them (the tensor core's additions truncate,
+  // which a long chain would show in an fp32 output).
+  const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.tm_cols / nbuf;
+  auto seg_blocks = [&](int n_kb) { return (n_kb + nseg - 1) / nseg; };
   pdl_trigger();
 
   // k-blocks of this CTA's part of a tile
@@ -252,50 +254,55 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   if (warp == 0) {
     if (!MANUAL && lane == 0) {
       const bool peer = CG == 2 && rank == 1;
-      int it = 0;
+      int it = 0, st = 0;  // loads issued; stage and its phase
+      uint32_t phase = 0;
       bool ok = true;
       pdl_wait();
       for (int t = unit; t < g.tiles && ok; t += units) {
         const Tile tl = tile_at(g, t);
         const ProductK& P = g.p[tl.p];
+        // (everything that the loop needs, in registers: an indexed parameter
+        // read per k-block would be the loop's critical path)
         const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
         const int brows = P.bn / CG;
-        const int n0 = P.gated ? tl.n * (P.bn / 2) : tl.n * P.bn + (CG == 2 ? (int)rank * brows : 0);
+        const bool gated = P.gated, amn = P.a_mn, bmn = P.b_mn;
+        const int n0 = gated ? tl.n * (P.bn / 2) : tl.n * P.bn + (CG == 2 ? (int)rank * brows : 0);
         const uint32_t bytes = (uint32_t)(kABytes + brows * BK * 2) * CG;
-        const int hi = k_hi(P);
-        for (int kb = k_lo(P); kb < hi; ++kb, ++it) {
-          const int s = it % stages;
-          if (it >= stages && !mbar_wait(&empty[s], (it / stages - 1) & 1, status, kStatusTimeoutTmaEmpty, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (!peer) mbar_arrive_expect_tx(&full[s], bytes);
-          const int q = kb >= P.kb0 ? 1 : 0, kk = (kb - (q ? P.kb0 : 0)) * BK;
-          uint8_t* sa = smem + (size_t)s * sbytes;
-          uint8_t* sb = sa + kABytes;
-          auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
-            if (peer)
-              tma_load_3d_pair(dst, map, cluster_addr(&full[s], 0), x, y, 0);
-            else
-              tma_load_3d(dst, map, &full[s], x, y, 0);
-          };
-          if (P.a_mn) {
-            load(&P.ma[q], sa, m0, kk);
-            load(&P.ma[q], sa + 8192, m0 + 64, kk);
-          } else {
-            load(&P.ma[q], sa, kk, m0);
-          }
-          if (P.gated) {  // columns: g then u (a pair: one CTA each)
-            if (CG == 2) {
-              load(&P.mb[rank], sb, kk, n0);
-            } else {
-              load(&P.mb[0], sb, kk, n0);
-              load(&P.mb[1], sb + brows / 2 * 128, kk, n0);
+        const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0;
+        for (int q = 0; q < 2 && ok; ++q) {  // operand pairs
+          const CUtensorMap* ma = &P.ma[q];
+          const CUtensorMap* mb = gated && CG == 2 ? &P.mb[rank] : &P.mb[q];
+          const CUtensorMap* mb1 = &P.mb[1];
+          const int end = q ? hi : min(hi, kb0);
+          for (int kb = q ? max(lo, kb0) : lo; kb < end; ++kb, ++it) {
+            if (it >= stages && !mbar_wait(&empty[st], phase ^ 1, status, kStatusTimeoutTmaEmpty, abort_flag)) {
+              ok = false;
+              break;
             }
-          } else if (P.b_mn) {
-            for (int j = 0; j < brows; j += 64) load(&P.mb[q], sb + j * 128, n0 + j, kk);
-          } else {
-            load(&P.mb[q], sb, kk, n0);
+            if (!peer) mbar_arrive_expect_tx(&full[st], bytes);
+            const int kk = (q ? kb - kb0 : kb) * BK;
+            uint8_t* sa = smem + (size_t)st * sbytes;
+            uint8_t* sb = sa + kABytes;
+            const uint32_t bar = peer ? cluster_addr(&full[st], 0) : smem_u32(&full[st]);
+            auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
+              if (CG == 2 && peer)
+                tma_load_3d_pair(dst, map, bar, x, y, 0);
+              else
+                tma_load_3d(dst, map, &full[st], x, y, 0);
+            };
+            if (amn) {
+              load(ma, sa, m0, kk);
+              load(ma, sa + 8192, m0 + 64, kk);
+            } else {
+              load(ma, sa, kk, m0);
+            }
+            if (bmn) {
+              for (int j = 0; j < brows; j += 64) load(mb, sb + j * 128, n0 + j, kk);
+            } else {
+              load(mb, sb, kk, n0);  // gated: g's rows, then u's (a pair: one CTA each)
+              if (CG == 1 && gated) load(mb1, sb + brows / 2 * 128, kk, n0);
+            }
+            if (++st == stages) st = 0, phase ^= 1;
           }
         }
       }
@@ -312,42 +319,45 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
     }
   } else if (warp == 1) {
     if (lane == 0 && rank * (CG - 1) == 0) {
-      int it = 0, lt = 0;
+      int st = 0, buf = 0, lt = 0;
+      uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int t = unit; t < g.tiles && ok; t += units, ++lt) {
         const ProductK& P = g.p[tile_at(g, t).p];
-        const int buf = lt & 1;
-        if (lt >= 2 && !mbar_wait(&acce[buf], (lt / 2 - 1) & 1, status, kStatusTimeoutAccum, abort_flag)) break;
+        if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * buf_cols;
-        const uint32_t idesc =
-            idesc_bf16_f32(BM * CG, P.bn) | (P.a_mn ? 1u << 15 : 0u) | (P.b_mn ? 1u << 16 : 0u);
         const bool amn = P.a_mn, bmn = P.b_mn;
+        const uint32_t bn = P.bn;
+        const uint32_t idesc = idesc_bf16_f32(BM * CG, bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
         const uint64_t sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;  // descriptor step per K = 16
-        const int lo = k_lo(P), hi = k_hi(P);
-        for (int kb = lo; kb < hi; ++kb, ++it) {
-          const int s = it % stages;
-          if (!mbar_wait(&full[s], (it / stages) & 1, status, kStatusTimeoutTmaFull, abort_flag)) {
+        const uint64_t da0 = smem_desc(0, amn), db0 = smem_desc(0, bmn);
+        const int n_kb = k_hi(P) - k_lo(P), seg = seg_blocks(n_kb);
+        uint32_t d = tmem + buf * buf_cols;
+        for (int kb = 0, in = 0; kb < n_kb; ++kb) {
+          if (!mbar_wait(&full[st], phase, status, kStatusTimeoutTmaFull, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + (size_t)s * sbytes);
-          const uint64_t da = smem_desc(a0, amn), db = smem_desc(a0 + kABytes, bmn);
+          const uint32_t a0 = smem_u32(smem) + (uint32_t)(st * sbytes);
+          // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
+          const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | ((a0 + kABytes) >> 4 & 0x3FFF);
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) {
-            const uint32_t acc = (kb > lo || k > 0) ? 1u : 0u;
+            const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
             if constexpr (CG == 2)
               tc_mma_bf16_pair(d, da + k * sa, db + k * sb, idesc, acc);
             else
               tc_mma_bf16(d, da + k * sa, db + k * sb, idesc, acc);
           }
           if constexpr (CG == 2) {
-            tc_commit_pair(smem_u32(&empty[s]));
-            tc_commit_pair(cluster_addr(&empty[s], 1));
+            tc_commit_pair(smem_u32(&empty[st]));
+            tc_commit_pair(cluster_addr(&empty[st], 1));
           } else {
-            tc_commit(&empty[s]);
+            tc_commit(&empty[st]);
           }
+          if (++st == stages) st = 0, phase ^= 1;
+          if (++in == seg) in = 0, d += bn;
         }
         if constexpr (CG == 2) {
           tc_commit_pair(smem_u32(&accf[buf]));
@@ -355,6 +365,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         } else {
           tc_commit(&accf[buf]);
         }
+        if (++buf == nbuf) buf = 0, bphase ^= 1;
       }
     }
     __syncwarp();
@@ -372,28 +383,43 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
       }
     }
     uint8_t* stg = sStg + quad * kStg;
-    int lt = 0;
-    for (int t = unit; t < g.tiles; t += units, ++lt) {
+    int buf = 0;
+    uint32_t bphase = 0;
+    for (int t = unit; t < g.tiles; t += units) {
       const Tile tl = tile_at(g, t);
       const ProductK& P = g.p[tl.p];
+      const OpEpi e = P.e;
+      const int bn = P.bn, pM = P.M, pN = P.N;
+      const bool gated = P.gated;
       const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
-      const int n0 = tl.n * (P.gated ? P.bn / 2 : P.bn);
-      const int buf = lt & 1;
-      const bool ok = mbar_wait(&accf[buf], (lt >> 1) & 1, status, kStatusTimeoutAccum, abort_flag);
+      const int n0 = tl.n * (gated ? bn / 2 : bn);
+      const int n_kb = k_hi(P) - k_lo(P), sg = seg_blocks(n_kb), segs = (n_kb + sg - 1) / sg;
+      const bool ok = mbar_wait(&accf[buf], bphase, status, kStatusTimeoutAccum, abort_flag);
       tc_fence_after();
       if (!ok) *abort_flag = 1;
       epi_sync();  // one decision for all four warps
       if (*abort_flag) break;
       const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * buf_cols;
       const int mw = m0 + quad * 32;
+      // 32 accumulator columns, the segments added
+      auto acc32 = [&](int c, float (&v)[32]) {
+        tmem_ld32(t_row + c, v);
+#pragma unroll 1
+        for (int k = 1; k < segs; ++k) {
+          float w[32];
+          tmem_ld32(t_row + k * bn + c, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += w[i];
+        }
+      };
       if (S > 1) {
         // leave the partial tile in the idle operand ring, chunk q of row r at q ^ (r & 7)
-        if (mw < P.M) {
+        if (mw < pM) {
           const int r = quad * 32 + lane;
-          uint8_t* row = smem + (size_t)r * P.bn * 4;
-          for (int c = 0; c < P.bn; c += 32) {
+          uint8_t* row = smem + (size_t)r * bn * 4;
+          for (int c = 0; c < bn; c += 32) {
             float v[32];
-            tmem_ld32(t_row + c, v);
+            acc32(c, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<float4*>(row + ((((c >> 2) + q) ^ (r & 7)) << 4)) =
@@ -402,15 +428,15 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         }
         break;  // one tile per cluster; the rest after the cluster barrier
       }
-      const int step = P.gated ? 32 : 64, width = P.gated ? P.bn / 2 : P.bn;
+      const int step = gated ? 32 : 64, width = gated ? bn / 2 : bn;
       for (int c = 0; c < width; c += step) {
         float v[32];
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          tmem_ld32(t_row + (P.gated ? c + h * (P.bn / 2) : c + 32 * h), v);
+          acc32(gated ? c + h * (bn / 2) : c + 32 * h, v);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(stg + stg_off(lane, 8 * h + q, P.gated)) =
+            *reinterpret_cast<float4*>(stg + stg_off(lane, 8 * h + q, gated)) =
                 make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
         if (c + step >= width) tc_fence_before();
@@ -421,27 +447,29 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
           else
             mbar_arrive(&acce[buf]);
         }
-        if (mw < P.M) {
-          if (P.gated) {
-            if (P.e.vec)
-              finish_vec<true>(P.e, stg, lane, mw, P.M, n0 + c, P.N);
+        if (mw < pM) {
+          if (gated) {
+            if (e.vec)
+              finish_vec<true>(e, stg, lane, mw, pM, n0 + c, pN);
             else
-              finish_any<true>(P.e, stg, lane, mw, P.M, n0 + c, P.N);
+              finish_any<true>(e, stg, lane, mw, pM, n0 + c, pN);
           } else {
-            if (P.e.vec)
-              finish_vec<false>(P.e, stg, lane, mw, P.M, n0 + c, P.N);
+            if (e.vec)
+              finish_vec<false>(e, stg, lane, mw, pM, n0 + c, pN);
             else
-              finish_any<false>(P.e, stg, lane, mw, P.M, n0 + c, P.N);
+              finish_any<false>(e, stg, lane, mw, pM, n0 + c, pN);
           }
         }
         __syncwarp();
       }
+      if (++buf == nbuf) buf = 0, bphase ^= 1;
     }
   } else if (MANUAL) {
     // ------------------------------------------------------------- loaders
     pdl_wait();
     const int tl_ = threadIdx.x - 192;
-    int it = 0;
+    int it = 0, s = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (int t = unit; t < g.tiles && ok; t += units) {
       const Tile tl = tile_at(g, t);
@@ -449,9 +477,8 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
       const int m0 = tl.m * BM, n0 = tl.n * (P.gated ? P.bn / 2 : P.bn);
       const int hi = k_hi(P);
       for (int kb = k_lo(P); kb < hi; ++kb, ++it) {
-        const int s = it % stages;
         // (one answer for the whole warp)
-        if (it >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (it / stages - 1) & 1, status,
+        if (it >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], phase ^ 1, status,
                                                                kStatusTimeoutTmaEmpty, abort_flag))) {
           ok = false;
           break;
@@ -491,6 +518,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == stages) s = 0, phase ^= 1;
       }
     }
   }
@@ -508,16 +536,17 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
 #pragma unroll
       for (int s = 0; s < 8; ++s) base[s] = s < S ? mapa_u32(smem_u32(smem), s) : 0u;
       const int te = threadIdx.x - 64;
+      const OpEpi e = P.e;
       if (P.gated) {
-        if (P.e.vec)
-          finish_split<false, true, 4>(P.e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+        if (e.vec)
+          finish_split<false, true, 4>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, true, 1>(P.e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, true, 1>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
       } else {
-        if (P.e.vec)
-          finish_split<false, false, 8>(P.e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+        if (e.vec)
+          finish_split<false, false, 8>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, false, 1>(P.e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, false, 1>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
       }
     }
   }
@@ -529,8 +558,8 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
     if (lane == 0) {  // the last commits have arrived before the tensor memory is freed
       int n = 0;
       for (int t = unit; t < g.tiles; t += units) ++n;
-      for (int l = max(0, n - 2); l < n; ++l)
-        mbar_wait(&accf[l & 1], (l >> 1) & 1, status, kStatusTimeoutDrain, nullptr);
+      for (int l = max(0, n - nbuf); l < n; ++l)
+        mbar_wait(&accf[l % nbuf], (l / nbuf) & 1, status, kStatusTimeoutDrain, nullptr);
     }
     __syncwarp();
   }
@@ -586,7 +615,11 @@ cudaError_t device_info(Device** out) {
 
 struct Plan {
   int cg, bn, split;
+  int seg;  // accumulator segments
 };
+// Longest chain of k-blocks in one accumulator when the output is fp32: 1536
+// products, about 8e-7 of the result in truncated additions (6144: 3e-6).
+constexpr int kChain = 24;
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Accumulator columns of product p's tiles under plan width bn.
@@ -600,7 +633,7 @@ int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, B
 // Estimated clocks of a plan: the busiest CTA (pair)'s k-blocks at the
 // measured cost of one, plus the parts that nothing overlaps.
 double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
-  const double per = pl.cg == 2 ? 560 : pl.bn == 256 ? 580 : pl.bn == 128 ? 380 : 270;
+  const double per = pl.cg == 2 ? (pl.bn == 256 ? 560 : 320) : pl.bn == 256 ? 580 : pl.bn == 128 ? 380 : 270;
   const int units = pl.cg == 2 ? d.pairs : d.sms;
   if (pl.split > 1) {
     const OpProduct& q = p[0];
@@ -628,19 +661,30 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
 }
 
 Plan choose(const OpProduct* p, int n, bool manual, const Device& d) {
-  Plan best{1, 128, 1};
+  Plan best{1, 128, 1, 1};
   double bc = 1e30;
+  int chain = 0;  // longest reduction that ends in fp32
+  for (int i = 0; i < n; ++i)
+    if (p[i].e.out_f32) chain = std::max(chain, k_blocks(p[i]));
   auto consider = [&](Plan pl) {
+    pl.seg = std::max(1, ceil_div(ceil_div(chain, pl.split), kChain));
+    if (pl.seg > 512 / pl.bn) {  // no tensor memory for so many: the narrowest tile takes what there is
+      if (pl.bn > 64) return;
+      pl.seg = 512 / pl.bn;
+    }
     const double c = plan_cost(p, n, pl, d);
     if (c < bc) bc = c, best = pl;
   };
   for (int bn : {256, 128, 64}) {
-    consider(Plan{1, bn, 1});
+    consider(Plan{1, bn, 1, 1});
     if (n == 1)
       for (int s = 2; s <= 8; ++s)
-        if (k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s});
+        if (k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s, 1});
   }
-  if (!manual) consider(Plan{2, 256, 1});
+  if (!manual) {
+    consider(Plan{2, 256, 1, 1});
+    consider(Plan{2, 128, 1, 1});
+  }
   return best;
 }
 
@@ -706,8 +750,10 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int 
   g.split = pl.split;
   g.stage_bytes = kABytes + bmax / pl.cg * BK * 2;
   g.stages = std::min(kMaxStages, (kSmemMax - kBarBytes - 4 * kStg) / g.stage_bytes);
+  g.nseg = pl.seg;
+  g.nbuf = pl.split == 1 && 2 * pl.seg * bmax <= 512 ? 2 : 1;
   g.tm_cols = 32;
-  while (g.tm_cols < 2 * bmax) g.tm_cols *= 2;
+  while (g.tm_cols < g.nbuf * pl.seg * bmax) g.tm_cols *= 2;
   const size_t smem = (size_t)g.stages * g.stage_bytes + 4 * kStg + kBarBytes;
 
   const int cluster = pl.cg == 2 ? 2 : pl.split;

@@ -98,63 +98,135 @@ __device__ __forceinline__ void act_and_grad(int act, float z, float& a, float& 
 }
 
 // ---------------------------------------------- E consecutive elements -----
-// p: first element (fp32 or bf16), 16-byte (bf16, E = 4: 8-byte) accesses
-// when E > 1, which the caller's alignment flag guarantees.
-template <int E>
-__device__ __forceinline__ void load_f32(const float* p, float (&v)[E]) {
-  if constexpr (E == 1) {
-    v[0] = *p;
-  } else {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const float4 t = reinterpret_cast<const float4*>(p)[i];
-      v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
-    }
-  }
-}
+// 16-byte (bf16, E = 4: 8-byte) accesses when E > 1, which the caller's
+// alignment flag guarantees.  Raw<T, E> holds loaded elements unconverted, so
+// that a batch of loads is in flight before the first is waited for (a
+// conversion, or a branch on the type, between two loads would wait for each).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <typename T, int E>
+struct Raw;
+template <>
+struct Raw<float, 1> {
+  float v;
+  __device__ __forceinline__ void zero() { v = 0.f; }
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ void get(float* o) const { o[0] = v; }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+  unsigned short v;
+  __device__ __forceinline__ void zero() { v = 0; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const unsigned short*>(p); }
+  __device__ __forceinline__ void get(float* o) const { o[0] = __uint_as_float((uint32_t)v << 16); }
+};
 template <int E>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&v)[E]) {
-  if constexpr (E == 1) {
-    v[0] = __bfloat162float(*p);
-  } else if constexpr (E == 4) {
-    const uint2 t = *reinterpret_cast<const uint2*>(p);
-    v[0] = bf16_lo(t.x), v[1] = bf16_hi(t.x), v[2] = bf16_lo(t.y), v[3] = bf16_hi(t.y);
-  } else {
-    static_assert(E == 8, "1, 4 or 8 elements");
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    v[0] = bf16_lo(t.x), v[1] = bf16_hi(t.x), v[2] = bf16_lo(t.y), v[3] = bf16_hi(t.y);
-    v[4] = bf16_lo(t.z), v[5] = bf16_hi(t.z), v[6] = bf16_lo(t.w), v[7] = bf16_hi(t.w);
+struct Raw<float, E> {
+  float4 v[E / 4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float* o) const {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) o[4 * i] = v[i].x, o[4 * i + 1] = v[i].y, o[4 * i + 2] = v[i].z, o[4 * i + 3] = v[i].w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* o) const {
+    o[0] = bf16_lo(v.x), o[1] = bf16_hi(v.x), o[2] = bf16_lo(v.y), o[3] = bf16_hi(v.y);
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* o) const {
+    o[0] = bf16_lo(v.x), o[1] = bf16_hi(v.x), o[2] = bf16_lo(v.y), o[3] = bf16_hi(v.y);
+    o[4] = bf16_lo(v.z), o[5] = bf16_hi(v.z), o[6] = bf16_lo(v.w), o[7] = bf16_hi(v.w);
+  }
+};
+
+template <int E>
+__device__ __forceinline__ void load_f32(const float* p, float (&v)[E]) {
+  Raw<float, E> r;
+  r.load(p);
+  r.get(v);
 }
 template <int E>
 __device__ __forceinline__ void load_any(const void* p, bool f32, size_t i, float (&v)[E]) {
-  if (f32)
+  if (f32) {
     load_f32<E>(reinterpret_cast<const float*>(p) + i, v);
+  } else {
+    Raw<__nv_bfloat16, E> r;
+    r.load(reinterpret_cast<const __nv_bfloat16*>(p) + i);
+    r.get(v);
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_to(float* d, const float* v) {
+  if constexpr (E == 1) {
+    *d = v[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k)
+      reinterpret_cast<float4*>(d)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_to(__nv_bfloat16* d, const float* v) {
+  if constexpr (E == 1)
+    *d = __float2bfloat16_rn(v[0]);
+  else if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   else
-    load_bf16<E>(reinterpret_cast<const __nv_bfloat16*>(p) + i, v);
+    *reinterpret_cast<uint4*>(d) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 template <int E>
 __device__ __forceinline__ void store_any(void* p, bool f32, size_t i, const float (&v)[E]) {
+  if (f32)
+    store_to<E>(reinterpret_cast<float*>(p) + i, v);
+  else
+    store_to<E>(reinterpret_cast<__nv_bfloat16*>(p) + i, v);
+}
+// n elements' groups of E at p + at(i), all requested before the first is converted.
+template <int E, int N, typename At>
+__device__ __forceinline__ void load_batch(const void* p, bool f32, At at, float (&v)[N][E]) {
   if (f32) {
-    float* d = reinterpret_cast<float*>(p) + i;
-    if constexpr (E == 1) {
-      *d = v[0];
-    } else {
+    Raw<float, E> r[N];
 #pragma unroll
-      for (int k = 0; k < E / 4; ++k)
-        reinterpret_cast<float4*>(d)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    for (int i = 0; i < N; ++i) {
+      const long long o = at(i);
+      if (o >= 0)
+        r[i].load(reinterpret_cast<const float*>(p) + o);
+      else
+        r[i].zero();
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].get(v[i]);
   } else {
-    __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(p) + i;
-    if constexpr (E == 1)
-      *d = __float2bfloat16_rn(v[0]);
-    else if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    else
-      *reinterpret_cast<uint4*>(d) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    Raw<__nv_bfloat16, E> r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long o = at(i);
+      if (o >= 0)
+        r[i].load(reinterpret_cast<const __nv_bfloat16*>(p) + o);
+      else
+        r[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].get(v[i]);
   }
 }
 

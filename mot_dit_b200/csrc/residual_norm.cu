@@ -18,6 +18,7 @@
 // rows (all of one sample), go to a partial array once, and a second kernel
 // adds the partials in order: no atomics, the same bits every time.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "op_epilogue.cuh"
@@ -45,54 +46,55 @@ template <int E>
 __device__ __forceinline__ int elem(int t, int tpr, int j) {
   return E == 8 ? (t + (j / 8) * tpr) * 8 + j % 8 : t + j * tpr;
 }
-template <int E, int NV>
-__device__ __forceinline__ void row_load(const void* p, bool f32, size_t row, int D, int t, int tpr, float (&v)[NV]) {
-  if constexpr (E == 8) {
+// A row's elements of this thread, unconverted (zero past the row's end).
+template <int E, int NV, typename T>
+struct Row {
+  Raw<T, E> r[NV / E];
+  __device__ __forceinline__ void load(const T* p, int D, int t, int tpr) {
 #pragma unroll
-    for (int k = 0; k < NV / 8; ++k) {
-      const int i = elem<8>(t, tpr, 8 * k);
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (i < D) load_any<8>(p, f32, row * D + i, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * k + j] = w[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = elem<1>(t, tpr, j);
-      float w[1] = {0.f};
-      if (i < D) load_any<1>(p, f32, row * D + i, w);
-      v[j] = w[0];
+    for (int k = 0; k < NV / E; ++k) {
+      const int i = elem<E>(t, tpr, E * k);
+      if (i < D)
+        r[k].load(p + i);
+      else
+        r[k].zero();
     }
   }
-}
-template <int E, int NV>
-__device__ __forceinline__ void row_store(void* p, bool f32, size_t row, int D, int t, int tpr, const float (&v)[NV]) {
-  if constexpr (E == 8) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int k = 0; k < NV / 8; ++k) {
-      const int i = elem<8>(t, tpr, 8 * k);
-      float w[8];
+    for (int k = 0; k < NV / E; ++k) r[k].zero();
+  }
+  __device__ __forceinline__ void get(float (&v)[NV]) const {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = v[8 * k + j];
-      if (i < D) store_any<8>(p, f32, row * D + i, w);
-    }
-  } else {
+    for (int k = 0; k < NV / E; ++k) r[k].get(v + E * k);
+  }
+};
+template <int E, int NV, typename T>
+__device__ __forceinline__ void row_store(T* p, int D, int t, int tpr, const float (&v)[NV]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = elem<1>(t, tpr, j);
-      const float w[1] = {v[j]};
-      if (i < D) store_any<1>(p, f32, row * D + i, w);
-    }
+  for (int k = 0; k < NV / E; ++k) {
+    const int i = elem<E>(t, tpr, E * k);
+    if (i < D) store_to<E>(p + i, v + E * k);
   }
 }
 // A column vector's elements of this thread (fill without one).
 template <int E, int NV>
 __device__ __forceinline__ void vec_load(const float* p, float fill, int D, int t, int tpr, float (&v)[NV]) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = fill;
+    return;
+  }
+  if (E == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    Row<8, NV, float> r;
+    r.load(p, D, t, tpr);
+    r.get(v);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = elem<E>(t, tpr, j);
-    v[j] = p && i < D ? p[i] : fill;
+    v[j] = i < D ? p[i] : 0.f;
   }
 }
 
@@ -138,22 +140,29 @@ __device__ __forceinline__ void coef(const ResNorm& a, int grp, int t, int tpr, 
   for (int j = 0; j < NV; ++j) w[j] *= x[j];
 }
 
-// Block: (tpr, rows); its rows are [M b / grid, M (b + 1) / grid).
-template <int E, int NV>
+// Block: (tpr, rows); its rows are [M b / grid, M (b + 1) / grid).  RT / CT:
+// the stream's and the compute type.
+template <int E, int NV, typename RT, typename CT>
 __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
   __shared__ float sh[2 * 8 * 32];  // (rows > 8 only when a row is within a warp)
-  const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y;
+  const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y, D = a.D;
   const int lo = (int)((long long)a.M * blockIdx.x / gridDim.x), hi = (int)((long long)a.M * (blockIdx.x + 1) / gridDim.x);
+  const RT* px = reinterpret_cast<const RT*>(a.x);
+  const CT* py = reinterpret_cast<const CT*>(a.y);
   pdl_trigger();
   pdl_wait();
   int phase = 0, grp = -1;
-  float mul[NV], add[NV], w[NV], x[NV], y[NV];
+  float mul[NV], add[NV], w[NV];
+  Row<E, NV, RT> rx;
+  Row<E, NV, CT> ryy;
   auto load = [&](int m) {
     if (m < hi) {
-      row_load<E, NV>(a.x, a.res_f32, m, a.D, t, tpr, x);
-      row_load<E, NV>(a.y, a.f32, m, a.D, t, tpr, y);
+      rx.load(px + (size_t)m * D, D, t, tpr);
+      ryy.load(py + (size_t)m * D, D, t, tpr);
     }
   };
+  rx.zero();
+  ryy.zero();
   load(lo + ry);
   for (int m0 = lo; m0 < hi; m0 += R) {
     const int m = m0 + ry;
@@ -162,8 +171,8 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
     if (gr != grp) coef<E, NV>(a, gr, t, tpr, mul, add, w);
     grp = gr;
     float v[NV], q[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = x[j], q[j] = y[j];
+    rx.get(v);
+    ryy.get(q);
     load(m + R);
     float s1[1] = {0.f};
     float rp = 1.f;
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) s1[0] += q[j] * q[j];
       row_sum<1>(s1, t, tpr, ry, R, sh, phase);
-      rp = 1.f / sqrtf(s1[0] / (float)a.D + kEps);
+      rp = 1.f / sqrtf(s1[0] / (float)D + kEps);
     }
     s1[0] = 0.f;
 #pragma unroll
@@ -180,19 +189,19 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
       s1[0] += v[j] * v[j];
     }
     row_sum<1>(s1, t, tpr, ry, R, sh, phase);
-    const float r = 1.f / sqrtf(s1[0] / (float)a.D + kEps);
+    const float r = 1.f / sqrtf(s1[0] / (float)D + kEps);
     if (live) {
-      row_store<E, NV>(a.s, a.res_f32, m, a.D, t, tpr, v);
+      row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, D, t, tpr, v);
 #pragma unroll
       for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
-      row_store<E, NV>(a.h, a.f32, m, a.D, t, tpr, v);
+      row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, D, t, tpr, v);
     }
   }
 }
 
 // Block: chunk blockIdx.x % chunks of the rows of sample blockIdx.x / chunks.  AHEAD: the next
 // row is requested early (the widest rows have no registers for it).
-template <int E, int NV, bool AHEAD>
+template <int E, int NV, bool AHEAD, typename RT, typename CT>
 __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a, int chunks) {
   extern __shared__ float dyn[];    // [rows][3][tpr NV] column sums of the row lanes (rows > 1)
   __shared__ float sh[2 * 6 * 8 * 32];
@@ -211,20 +220,20 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
   float sa[NV], sb[NV], sq[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) sa[j] = sb[j] = sq[j] = 0.f;
-  float xs[NV], xy[NV], xd[NV], xh[NV];
+  Row<E, NV, RT> xs, xd;
+  Row<E, NV, CT> xy, xh;
   auto load = [&](int m) {
     if (m < hi) {
-      row_load<E, NV>(f.x, f.res_f32, m, D, t, tpr, xs);
-      row_load<E, NV>(f.y, f.f32, m, D, t, tpr, xy);
-      row_load<E, NV>(a.dh, f.f32, m, D, t, tpr, xh);
-      if (a.ds) row_load<E, NV>(a.ds, f.res_f32, m, D, t, tpr, xd);
+      const size_t o = (size_t)m * D;
+      xs.load(reinterpret_cast<const RT*>(f.x) + o, D, t, tpr);
+      xy.load(reinterpret_cast<const CT*>(f.y) + o, D, t, tpr);
+      xh.load(reinterpret_cast<const CT*>(a.dh) + o, D, t, tpr);
+      if (a.ds) xd.load(reinterpret_cast<const RT*>(a.ds) + o, D, t, tpr);
     } else {  // (a row lane past the chunk's end: adds nothing)
-#pragma unroll
-      for (int j = 0; j < NV; ++j) xs[j] = xy[j] = xh[j] = xd[j] = 0.f;
+      xs.zero(), xy.zero(), xh.zero(), xd.zero();
     }
   };
-#pragma unroll
-  for (int j = 0; j < NV; ++j) xd[j] = 0.f;
+  xd.zero();
   if (AHEAD) load(lo + ry);
   const float inv = 1.f / (float)D;
   for (int m0 = lo; m0 < hi; m0 += R) {
@@ -232,8 +241,7 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
     const bool live = m < hi;
     if (!AHEAD) load(m);
     float s[NV], y[NV], ds[NV], dh[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) s[j] = xs[j], y[j] = xy[j], ds[j] = xd[j], dh[j] = xh[j];
+    xs.get(s), xy.get(y), xd.get(ds), xh.get(dh);
     if (AHEAD) load(m + R);
     float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -265,8 +273,8 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
       dh[j] = f.post ? rp * (dv * w[j] - y[j] * cy) : dv * w[j];
     }
     if (live) {
-      row_store<E, NV>(a.dx, f.res_f32, m, D, t, tpr, ds);
-      row_store<E, NV>(a.dy, f.f32, m, D, t, tpr, dh);
+      row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, ds);
+      row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, dh);
     }
   }
   if (!a.part) return;
@@ -373,31 +381,47 @@ int grad_chunks(int M, int D, int rpg) {
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <int E, int NV>
+template <int E, int NV, typename RT, typename CT>
 cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const int tpr = row_threads(a.D, NV), R = rows_at_once(tpr);
   int dev = 0, sms = 148, per = 1;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, res_norm_kernel<E, NV>, tpr * R, 0)) != cudaSuccess)
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, res_norm_kernel<E, NV, RT, CT>, tpr * R, 0)) != cudaSuccess)
     return e;
   const int grid = std::max(1, std::min((a.M + R - 1) / R, sms * std::max(1, per)));
-  return launch_k(res_norm_kernel<E, NV>, dim3(grid), dim3(tpr, R), 0, s, a);
+  return launch_k(res_norm_kernel<E, NV, RT, CT>, dim3(grid), dim3(tpr, R), 0, s, a);
 }
-template <int E, int NV>
+template <int E, int NV, typename RT, typename CT>
 cudaError_t run_bwd(const ResNormGrad& a, int chunks, int groups, cudaStream_t s) {
   const int tpr = row_threads(a.f.D, NV), R = rows_at_once(tpr);
   const size_t smem = R > 1 && a.part ? (size_t)R * 3 * tpr * NV * 4 : 0;
-  return launch_k(res_norm_grad_kernel<E, NV, NV == 8>, dim3((unsigned)chunks * groups), dim3(tpr, R), smem, s, a, chunks);
+  return launch_k(res_norm_grad_kernel<E, NV, NV == 8, RT, CT>, dim3((unsigned)chunks * groups), dim3(tpr, R), smem, s, a,
+                  chunks);
+}
+// f(E, NV, RT, CT) for a call's alignment, width and types.
+template <typename F>
+cudaError_t by_form(bool vec, int D, bool res_f32, bool f32, F f) {
+  auto types = [&](auto e, auto nv) {
+    if (f32) return f(e, nv, float{}, float{});
+    return res_f32 ? f(e, nv, float{}, __nv_bfloat16{}) : f(e, nv, __nv_bfloat16{}, __nv_bfloat16{});
+  };
+  using std::integral_constant;
+  if (elems(D) == 8)
+    return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 8>{})
+               : types(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 16>{})
+             : types(integral_constant<int, 1>{}, integral_constant<int, 16>{});
 }
 
 }  // namespace
 
 cudaError_t launch_res_norm(const ResNorm& a, cudaStream_t s) {
   const bool v = a.D % 8 == 0 && aligned(a.x) && aligned(a.y) && aligned(a.s) && aligned(a.h);
-  if (elems(a.D) == 8) return v ? run_fwd<8, 8>(a, s) : run_fwd<1, 8>(a, s);
-  return v ? run_fwd<8, 16>(a, s) : run_fwd<1, 16>(a, s);
+  return by_form(v, a.D, a.res_f32, a.f32, [&](auto e, auto nv, auto rt, auto ct) {
+    return run_fwd<decltype(e)::value, decltype(nv)::value, decltype(rt), decltype(ct)>(a, s);
+  });
 }
 
 size_t res_norm_part_floats(int M, int D, int rpg) {
@@ -409,11 +433,9 @@ cudaError_t launch_res_norm_grad(const ResNormGrad& a, cudaStream_t s) {
   const ResNorm& f = a.f;
   const int groups = (f.M + f.rows_per_group - 1) / f.rows_per_group, chunks = grad_chunks(f.M, f.D, f.rows_per_group);
   const bool v = f.D % 8 == 0 && aligned(f.x) && aligned(f.y) && aligned(a.ds) && aligned(a.dh) && aligned(a.dx) && aligned(a.dy);
-  cudaError_t e;
-  if (elems(f.D) == 8)
-    e = v ? run_bwd<8, 8>(a, chunks, groups, s) : run_bwd<1, 8>(a, chunks, groups, s);
-  else
-    e = v ? run_bwd<8, 16>(a, chunks, groups, s) : run_bwd<1, 16>(a, chunks, groups, s);
+  const cudaError_t e = by_form(v, f.D, f.res_f32, f.f32, [&](auto e_, auto nv, auto rt, auto ct) {
+    return run_bwd<decltype(e_)::value, decltype(nv)::value, decltype(rt), decltype(ct)>(a, chunks, groups, s);
+  });
   if (e != cudaSuccess || !a.part) return e;
   return launch_k(res_norm_sum_kernel, dim3((f.D + 31) / 32), dim3(32, 32), 0, s, a, groups, chunks);
 }
