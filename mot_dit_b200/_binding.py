@@ -380,7 +380,15 @@ def op_attention_noalloc(q, k, v, out, B, H, Lq, Lk, Lcache, splits, stream=None
 
 
 # ------------------------------- feed-forward and residual-norm operators ---
-_TORCH_TYPES = {FP32: "torch.float32", BF16: "torch.bfloat16"}
+_torch = None
+_TORCH_TYPES = ()
+
+
+def _load_torch():
+    global _torch, _TORCH_TYPES
+    import torch
+    _TORCH_TYPES = (torch.float32, torch.bfloat16)  # indexed by wam_dtype
+    _torch = torch
 
 
 class _Args:
@@ -389,28 +397,44 @@ class _Args:
     and element count, on the current device.  None and raw integer addresses
     pass through unchecked."""
 
-    def __init__(self, where: str):
-        self.where = where
-        self.device = None
+    __slots__ = ("where", "device")
 
-    def __call__(self, name: str, x, dtype: int, n: int, rows=None):
-        """rows: (count, width, stride) of a table whose rows lie `stride` apart."""
+    def __init__(self, where: str):
+        if _torch is None:
+            _load_torch()
+        self.where = where
+        self.device = -2
+
+    def __call__(self, name: str, x, dtype: int, n: int):
         if x is None or isinstance(x, int):
             return x
-        if self.device is None:
-            import torch
-            self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
-        if rows is None or rows[2] == rows[1] or rows[0] == 1:
-            shape_ok = x.is_contiguous() and x.numel() == n
-        else:
-            shape_ok = x.dim() == 2 and tuple(x.shape) == rows[:2] and x.stride() == (rows[2], 1)
-        if not shape_ok and rows is not None and rows[0] == 1:  # one vector of a wider table
-            shape_ok = x.numel() == n and x.stride(-1) == 1
-        if not (shape_ok and x.is_cuda and x.device.index == self.device and str(x.dtype) == _TORCH_TYPES.get(dtype)):
-            want = f"{n} elements" if rows is None else f"{rows[0]} rows of {rows[1]}, {rows[2]} apart"
-            raise WamError(1, self.where, f"{name}: need a contiguous {_TORCH_TYPES.get(dtype)} tensor on the current "
-                           f"device, {want}; got {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
+        if not (x.is_cuda and dtype in (FP32, BF16) and x.dtype is _TORCH_TYPES[dtype] and x.numel() == n
+                and x.is_contiguous() and self._here(x)):
+            self._refuse(name, x, dtype, f"{n} elements")
         return x.data_ptr()
+
+    def table(self, name: str, x, rows: int, width: int, stride: int):
+        """fp32 rows of `width` elements, `stride` apart."""
+        if x is None or isinstance(x, int):
+            return x
+        ok = x.is_cuda and x.dtype is _TORCH_TYPES[FP32] and x.numel() == rows * width and self._here(x)
+        if ok and rows > 1:
+            ok = x.dim() == 2 and x.size(0) == rows and x.stride(0) == stride and (x.stride(1) == 1 or width == 1)
+        elif ok:
+            ok = x.stride(-1) == 1 or width == 1
+        if not ok:
+            self._refuse(name, x, FP32, f"{rows} rows of {width}, {stride} apart")
+        return x.data_ptr()
+
+    def _here(self, x) -> bool:
+        if self.device == -2:
+            self.device = _torch.cuda.current_device()
+        return x.get_device() == self.device
+
+    def _refuse(self, name, x, dtype, want):
+        kind = _TORCH_TYPES[dtype] if dtype in (FP32, BF16) else dtype
+        raise WamError(1, self.where, f"{name}: need a contiguous {kind} tensor on the current device, {want}; "
+                       f"got {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
 
     def workspace(self, x, need: int):
         """(pointer, bytes) of a workspace tensor of any type (an integer
@@ -419,8 +443,8 @@ class _Args:
             return None, 0
         if isinstance(x, int):
             return x, need
-        if not (x.is_cuda and x.is_contiguous()):
-            raise WamError(1, self.where, "workspace: need a contiguous CUDA tensor")
+        if not (x.is_cuda and x.is_contiguous() and self._here(x)):
+            raise WamError(1, self.where, "workspace: need a contiguous CUDA tensor on the current device")
         return x.data_ptr(), x.numel() * x.element_size()
 
 
@@ -502,13 +526,12 @@ def op_residual_norm(dtype, x, y, s, h, M, D, post_norm=False, post_gain=None, g
     """s = alpha x + gate p, p = y or post_gain rms(y); h = rms(s) gain (1 + scale)
     + shift (wam_op_residual_norm).  s may be x, h may be y."""
     where, ld = "wam_op_residual_norm", ld_mod or D
-    c, rows = _Args(where), (_groups(M, rows_per_group), D, ld)
-    n = rows[0] * D
+    c, G = _Args(where), _groups(M, rows_per_group)
     _done(lib().wam_op_residual_norm(dtype, res_dtype, c("x", x, res_dtype, M * D), c("y", y, dtype, M * D),
                                      c("s", s, res_dtype, M * D), c("h", h, dtype, M * D), M, D, alpha, int(post_norm),
-                                     c("post_gain", post_gain, FP32, D), c("gate", gate, FP32, n, rows),
-                                     c("gain", gain, FP32, D), c("scale", scale, FP32, n, rows),
-                                     c("shift", shift, FP32, n, rows), rows_per_group, ld, _stream(stream)), where)
+                                     c("post_gain", post_gain, FP32, D), c.table("gate", gate, G, D, ld),
+                                     c("gain", gain, FP32, D), c.table("scale", scale, G, D, ld),
+                                     c.table("shift", shift, G, D, ld), rows_per_group, ld, _stream(stream)), where)
 
 
 def op_residual_norm_workspace(M, D, rows_per_group=0) -> int:
@@ -525,13 +548,12 @@ def op_residual_norm_backward(dtype, s, y, ds, dh, dx, dy, M, D, post_norm=False
     None (zero), every parameter gradient too (not computed).  dx may be ds or
     s, dy may be dh or y."""
     where, ld = "wam_op_residual_norm_backward", ld_mod or D
-    c, rows = _Args(where), (_groups(M, rows_per_group), D, ld)
-    n = rows[0] * D
+    c, G = _Args(where), _groups(M, rows_per_group)
     ws, nb = c.workspace(workspace, 1 << 62)
     _done(lib().wam_op_residual_norm_backward(
         dtype, res_dtype, c("s", s, res_dtype, M * D), c("y", y, dtype, M * D), c("ds", ds, res_dtype, M * D),
         c("dh", dh, dtype, M * D), c("dx", dx, res_dtype, M * D), c("dy", dy, dtype, M * D), M, D, alpha, int(post_norm),
-        c("post_gain", post_gain, FP32, D), c("gate", gate, FP32, n, rows), c("gain", gain, FP32, D),
-        c("scale", scale, FP32, n, rows), rows_per_group, ld, c("dpost_gain", dpost_gain, FP32, D),
-        c("dgate", dgate, FP32, n), c("dgain", dgain, FP32, D), c("dscale", dscale, FP32, n),
-        c("dshift", dshift, FP32, n), ws, nb, _stream(stream)), where)
+        c("post_gain", post_gain, FP32, D), c.table("gate", gate, G, D, ld), c("gain", gain, FP32, D),
+        c.table("scale", scale, G, D, ld), rows_per_group, ld, c("dpost_gain", dpost_gain, FP32, D),
+        c("dgate", dgate, FP32, G * D), c("dgain", dgain, FP32, D), c("dscale", dscale, FP32, G * D),
+        c("dshift", dshift, FP32, G * D), ws, nb, _stream(stream)), where)

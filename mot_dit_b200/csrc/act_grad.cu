@@ -20,9 +20,9 @@ constexpr int kRows = 8;    // row lanes of a block
 
 // T: the compute type, DY: the incoming gradient's.
 template <int E, bool GATED, typename T, typename DY>
-__global__ void __launch_bounds__(32 * kRows) act_grad_kernel(const ActGrad a) {
+__global__ void __launch_bounds__(32 * kRows, 4) act_grad_kernel(const ActGrad a) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int kAhead = E == 1 ? 8 : 4;  // rows a thread has in flight
+  constexpr int kAhead = E == 1 ? 8 : E == 4 ? 4 : 2;  // rows a thread has in flight
   __shared__ float sh[GATED ? 2 : 1][kRows][32 * E];
   const int tx = threadIdx.x, ty = threadIdx.y;
   const int n = (blockIdx.x * 32 + tx) * E, chunk = blockIdx.y;
@@ -135,9 +135,12 @@ cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s) {
   return launch_k(col_sum_kernel, dim3((sums[0].cols + 127) / 128, n), dim3(128), 0, s, sums[0], sums[n - 1]);
 }
 
-// At most 64 chunks (the partial sums stay small against the matrices), each
-// of at least 16 rows.
-int act_grad_chunks(int M) { return std::max(1, std::min(64, (M + 15) / 16)); }
+// Two full waves of blocks at four an SM, chunks of at least 16 rows, and no
+// more than 128 (their sums are added one after another).
+int act_grad_chunks(int M, int N, bool f32) {
+  const int e = f32 ? (N % 4 ? 1 : 4) : (N % 8 ? 1 : 8), cols = (N + 32 * e - 1) / (32 * e);
+  return std::max(1, std::min({(1184 + cols - 1) / cols, (M + 15) / 16, 128}));
+}
 
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };

@@ -30,7 +30,7 @@
 //    same swizzled layout; the rest of the kernel does not change.
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warps
-// 2..5 epilogue (warp w reads TMEM lanes 32 (w % 4) ..), MANUAL: warps 6..9
+// 2..9 epilogue (warp w reads TMEM lanes 32 (w % 4) ..), MANUAL: warps 10..13
 // loaders.  No load is multicast.  Every wait is bounded (op_gemm_status).
 #include <algorithm>
 #include <atomic>
@@ -45,7 +45,10 @@ namespace {
 constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int kABytes = BM * BK * 2;
-constexpr int kStg = 32 * 64 * 4;  // staging of one epilogue warp: 32 rows x 64 fp32
+constexpr int kEpiWarps = 8;       // two per 32-row quarter of the tile, on alternate 32-column chunks
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kLoaders = 128;      // MANUAL: loader threads
+constexpr int kStg = 32 * 32 * 4;  // staging of one epilogue warp: 32 rows x 32 fp32
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 232448;
 constexpr int kMaxStages = 12;
@@ -68,6 +71,7 @@ struct GemmArgs {
   OpColSum sums[2];
   int np, n_sums, tiles;
   int stages, stage_bytes;
+  int subs, sub_bytes;  // k-blocks of a full stage, and the bytes of one
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
   int nbuf, nseg;  // accumulator buffers, and segments of each
   int tm_cols;  // tensor-memory columns to allocate
@@ -88,6 +92,28 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t) {
   return r;
 }
 
+// Arrive on the barrier at this offset in both CTAs of the pair once every
+// pair MMA issued so far by this thread completes.
+__device__ __forceinline__ void tc_commit_both(uint32_t addr) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(addr),
+      "h"((unsigned short)3)
+      : "memory");
+}
+
+// One thread of a converged warp.  (The compiler recognises the election and
+// issues the thread's TMA and MMA instructions without guarding against
+// several active lanes.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn) {
   // K-major: rows of 64 reduction elements, 8-row groups 1024 B apart.
   // MN-major: rows of 64 output elements, one row per reduction index; 8-row
@@ -101,91 +127,131 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn) {
   return d;
 }
 
-// Byte offset of 16-byte chunk q (0..15) of staging row r: rows of 256 bytes,
-// chunks permuted so that neither the row-per-lane writes nor the eight-
-// lanes-per-row reads meet a bank twice (gated: chunk q and q + 8 are read
-// by one lane; else chunks 2 c and 2 c + 1).
-__device__ __forceinline__ int stg_off(int r, int q, bool gated) {
-  const int pos = gated ? (((q & 7) ^ (r & 7)) | (q & 8)) : (((q >> 1) ^ (r & 7)) | ((q & 1) << 3));
-  return r * 256 + pos * 16;
+// ---- output of one warp: 32 rows (one per lane) x 32 columns, through the
+// warp's staging so that global accesses run along rows.  Staging rows are 64
+// (bf16) or 128 (fp32) bytes, their 16-byte chunks permuted so that neither
+// the row-per-lane writes nor the chunk-per-lane reads meet a bank twice.
+__device__ __forceinline__ uint4* stg16(uint8_t* stg, int r, int q) {
+  return reinterpret_cast<uint4*>(stg + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
-
-// 64 staged columns of 32 rows -> the output.  Eight lanes share a row, eight
-// (gated: four and four) columns each.
-template <bool GATED>
-__device__ __forceinline__ void finish_vec(const OpEpi& e, const uint8_t* stg, int lane, int m0, int M, int n0, int N) {
-  constexpr int E = GATED ? 4 : 8;
-  const int cg = lane & 7, n = n0 + cg * E;
-  if (n >= N) return;
-  float b[E], b2[E];
-  epi_bias<E>(e.bias, n, b);
-  if (GATED) epi_bias<E>(e.bias2, n, b2);
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    float r[4][E];
-    if (!GATED && e.res) {
-      load_batch<E, 4>(e.res, e.out_f32, [&](int i) {
-        const int m = m0 + (4 * h + i) * 4 + (lane >> 3);
-        return m < M ? (long long)m * e.ld + n : -1ll;
-      }, r);
-    }
+__device__ __forceinline__ float4* stg32(uint8_t* stg, int r, int q) {
+  return reinterpret_cast<float4*>(stg + r * 128 + ((q ^ (r & 7)) << 4));
+}
+struct Window {
+  int m0, M, n0, N, ld;
+  int vec;
+};
+__device__ __forceinline__ void out_bf16(const float (&v)[32], void* out, const Window& w, uint8_t* stg, int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *stg16(stg, lane, q) = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                                      pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+  __syncwarp();
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
+  if (w.vec) {
+    const int q = lane & 3, n = w.n0 + 8 * q;
+    __nv_bfloat16* p = o + (size_t)(w.m0 + (lane >> 2)) * w.ld + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int rr = (4 * h + i) * 4 + (lane >> 3), m = m0 + rr;
-      const int q0 = GATED ? cg : 2 * cg, q1 = GATED ? cg + 8 : 2 * cg + 1;
-      const float4 x = *reinterpret_cast<const float4*>(stg + stg_off(rr, q0, GATED));
-      const float4 y = *reinterpret_cast<const float4*>(stg + stg_off(rr, q1, GATED));
-      if (m >= M) continue;
-      const size_t at = (size_t)m * e.ld + n;
-      if constexpr (GATED) {
-        float g[4] = {x.x, x.y, x.z, x.w}, u[4] = {y.x, y.y, y.z, y.w};
-        epi_gated<false, 4>(e, at, g, u, b, b2);
-      } else {
-        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        epi_linear<false, 8>(e, at, v, b, r[i]);
-      }
+      const int r = 8 * i + (lane >> 2);
+      const uint4 x = *stg16(stg, r, q);
+      if (w.m0 + r < w.M && n < w.N) *reinterpret_cast<uint4*>(p + (size_t)(8 * i) * w.ld) = x;
+    }
+  } else {
+    const int n = w.n0 + lane, rows = min(32, w.M - w.m0);
+    unsigned short* p = reinterpret_cast<unsigned short*>(o) + (size_t)w.m0 * w.ld + n;
+    if (n < w.N) {
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r, p += w.ld) *p = reinterpret_cast<const unsigned short*>(stg16(stg, r, lane >> 3))[lane & 7];
     }
   }
+  __syncwarp();
 }
-// The same for outputs whose rows are not 16-byte aligned: a row at a time,
-// lanes on consecutive columns.
-template <bool GATED>
-__device__ __forceinline__ void finish_any(const OpEpi& e, const uint8_t* stg, int lane, int m0, int M, int n0, int N) {
-  const int rows = min(32, M - m0);
-#pragma unroll 1
-  for (int h = 0; h < (GATED ? 1 : 2); ++h) {
-    const int c = 32 * h + lane, n = n0 + c;
-    if (n >= N) continue;
-    float b[1], b2[1];
-    epi_bias<1>(e.bias, n, b);
-    if (GATED) epi_bias<1>(e.bias2, n, b2);
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      float res[8][1];
-      if (!GATED && e.res)
-        load_batch<1, 8>(e.res, e.out_f32,
-                         [&](int i) { return r0 + i < rows ? (long long)(m0 + r0 + i) * e.ld + n : -1ll; }, res);
+// The residual's elements that this lane will add (requested before the
+// accumulator is read).
+template <typename T>
+struct ResidualVec {
+  Raw<T, 4> r[8];
+  __device__ __forceinline__ void load(const void* res, const Window& w, int lane) {
+    const int n = w.n0 + 4 * (lane & 7);
+    const T* p = reinterpret_cast<const T*>(res) + (size_t)(w.m0 + (lane >> 3)) * w.ld + n;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i;
-        if (r >= rows) continue;
-        float v[1] = {*reinterpret_cast<const float*>(stg + stg_off(r, c >> 2, GATED) + (c & 3) * 4)};
-        const size_t at = (size_t)(m0 + r) * e.ld + n;
-        if constexpr (GATED) {
-          float u[1] = {*reinterpret_cast<const float*>(stg + stg_off(r, (c >> 2) + 8, GATED) + (c & 3) * 4)};
-          epi_gated<false, 1>(e, at, v, u, b, b2);
-        } else {
-          epi_linear<false, 1>(e, at, v, b, res[i]);
+    for (int i = 0; i < 8; ++i)
+      if (w.m0 + 4 * i + (lane >> 3) < w.M && n < w.N) r[i].load(p + (size_t)(4 * i) * w.ld);
+  }
+};
+// v (+ residual) as T.
+template <typename T>
+__device__ __forceinline__ void out_stream(const float (&v)[32], void* out, const void* res, const ResidualVec<T>& rv,
+                                           const Window& w, uint8_t* stg, int lane) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) *stg32(stg, lane, q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+  T* o = reinterpret_cast<T*>(out);
+  if (w.vec) {
+    const int q = lane & 7, n = w.n0 + 4 * q;
+    T* p = o + (size_t)(w.m0 + (lane >> 3)) * w.ld + n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const float4 x = *stg32(stg, r, q);
+      float y[4] = {x.x, x.y, x.z, x.w};
+      if (w.m0 + r < w.M && n < w.N) {
+        if (res) {
+          float z[4];
+          rv.r[i].get(z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] += z[j];
+        }
+        store_to<4>(p + (size_t)(4 * i) * w.ld, y);
+      }
+    }
+  } else {
+    const int n = w.n0 + lane, rows = min(32, w.M - w.m0);
+    T* p = o + (size_t)w.m0 * w.ld + n;
+    const T* pr = reinterpret_cast<const T*>(res) + (size_t)w.m0 * w.ld + n;
+    if (n < w.N) {
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        Raw<T, 1> z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[i].zero();
+          if (res && r0 + i < rows) z[i].load(pr + (size_t)(r0 + i) * w.ld);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float y[1];
+          z[i].get(y);
+          y[0] += reinterpret_cast<const float*>(stg32(stg, r0 + i, lane >> 2))[lane & 3];
+          if (r0 + i < rows) store_to<1>(p + (size_t)(r0 + i) * w.ld, y);
         }
       }
     }
   }
+  __syncwarp();
+}
+// Adds bias[n0 ..] to 32 columns (all lanes read the same words).
+__device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int n0, int N, int vec) {
+  if (!bias) return;
+  if (vec && n0 + 32 <= N) {
+    float4 b[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) b[q] = __ldg(reinterpret_cast<const float4*>(bias + n0) + q);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[4 * q] += b[q].x, v[4 * q + 1] += b[q].y, v[4 * q + 2] += b[q].z, v[4 * q + 3] += b[q].w;
+  } else {
+    float b[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) b[j] = n0 + j < N ? __ldg(bias + n0 + j) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += b[j];
+  }
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int CG, bool MANUAL>
-__global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __grid_constant__ GemmArgs g) {
+__global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op_gemm_kernel(const __grid_constant__ GemmArgs g) {
   static_assert(CG == 1 || !MANUAL, "the loader warps serve single CTAs");
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle is a function of the address bits
@@ -194,7 +260,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   }
   const int stages = g.stages, sbytes = g.stage_bytes;
   uint8_t* sStg = smem + (size_t)stages * sbytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + 4 * kStg);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + kEpiWarps * kStg);
   uint64_t* empty = full + kMaxStages;
   uint64_t* accf = empty + kMaxStages;
   uint64_t* acce = accf + 2;
@@ -202,7 +268,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   unsigned* status = &g_op_status;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = g.split;
   const uint32_t rank = (CG == 2 || S > 1) ? cluster_rank() : 0u;
   const int unit = CG == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x / S;
@@ -215,7 +281,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], CG == 2 && rank == 0 ? 8 : 4);
+      mbar_init(&acce[b], CG == 2 && rank == 0 ? 2 * kEpiWarps : kEpiWarps);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -244,7 +310,9 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   // k-blocks, and the epilogue adds them (the tensor core's additions truncate,
   // which a long chain would show in an fp32 output).
   const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.tm_cols / nbuf;
-  auto seg_blocks = [&](int n_kb) { return (n_kb + nseg - 1) / nseg; };
+  auto seg_blocks = [&](int n_kb) {  // (whole stages)
+    return ((n_kb + nseg - 1) / nseg + g.subs - 1) / g.subs * g.subs;
+  };
   pdl_trigger();
 
   // k-blocks of this CTA's part of a tile
@@ -252,10 +320,12 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   auto k_hi = [&](const ProductK& P) { return S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb; };
 
   if (warp == 0) {
-    if (!MANUAL && lane == 0) {
+    if (!MANUAL && elect_one()) {
       const bool peer = CG == 2 && rank == 1;
-      int it = 0, st = 0;  // loads issued; stage and its phase
+      int it = 0, st = 0;  // stages filled; the next one and its phase
       uint32_t phase = 0;
+      // a pair's stage completes on rank 0's barrier, for both CTAs' bytes
+      const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : 0u;
       bool ok = true;
       pdl_wait();
       for (int t = unit; t < g.tiles && ok; t += units) {
@@ -274,33 +344,36 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
           const CUtensorMap* mb = gated && CG == 2 ? &P.mb[rank] : &P.mb[q];
           const CUtensorMap* mb1 = &P.mb[1];
           const int end = q ? hi : min(hi, kb0);
-          for (int kb = q ? max(lo, kb0) : lo; kb < end; ++kb, ++it) {
+          for (int kb = q ? max(lo, kb0) : lo; kb < end; ++it) {
             if (it >= stages && !mbar_wait(&empty[st], phase ^ 1, status, kStatusTimeoutTmaEmpty, abort_flag)) {
               ok = false;
               break;
             }
-            if (!peer) mbar_arrive_expect_tx(&full[st], bytes);
-            const int kk = (q ? kb - kb0 : kb) * BK;
+            const int ns = min(g.subs, end - kb);
+            if (!peer) mbar_arrive_expect_tx(&full[st], bytes * ns);
             uint8_t* sa = smem + (size_t)st * sbytes;
-            uint8_t* sb = sa + kABytes;
-            const uint32_t bar = peer ? cluster_addr(&full[st], 0) : smem_u32(&full[st]);
+            const uint32_t bar = full0 + 8 * st;
             auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
-              if (CG == 2 && peer)
+              if (CG == 2)
                 tma_load_3d_pair(dst, map, bar, x, y, 0);
               else
                 tma_load_3d(dst, map, &full[st], x, y, 0);
             };
-            if (amn) {
-              load(ma, sa, m0, kk);
-              load(ma, sa + 8192, m0 + 64, kk);
-            } else {
-              load(ma, sa, kk, m0);
-            }
-            if (bmn) {
-              for (int j = 0; j < brows; j += 64) load(mb, sb + j * 128, n0 + j, kk);
-            } else {
-              load(mb, sb, kk, n0);  // gated: g's rows, then u's (a pair: one CTA each)
-              if (CG == 1 && gated) load(mb1, sb + brows / 2 * 128, kk, n0);
+            for (int i = 0; i < ns; ++i, ++kb, sa += g.sub_bytes) {
+              const int kk = (q ? kb - kb0 : kb) * BK;
+              uint8_t* sb = sa + kABytes;
+              if (amn) {
+                load(ma, sa, m0, kk);
+                load(ma, sa + 8192, m0 + 64, kk);
+              } else {
+                load(ma, sa, kk, m0);
+              }
+              if (bmn) {
+                for (int j = 0; j < brows; j += 64) load(mb, sb + j * 128, n0 + j, kk);
+              } else {
+                load(mb, sb, kk, n0);  // gated: g's rows, then u's (a pair: one CTA each)
+                if (CG == 1 && gated) load(mb1, sb + brows / 2 * 128, kk, n0);
+              }
             }
             if (++st == stages) st = 0, phase ^= 1;
           }
@@ -318,7 +391,9 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank * (CG - 1) == 0) {
+    if (rank * (CG - 1) == 0 && elect_one()) {
+      const int subs = g.subs, sub_bytes = g.sub_bytes;
+      const uint32_t smem0 = smem_u32(smem);
       int st = 0, buf = 0, lt = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
@@ -331,58 +406,58 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         const uint32_t idesc = idesc_bf16_f32(BM * CG, bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
         const uint64_t sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;  // descriptor step per K = 16
         const uint64_t da0 = smem_desc(0, amn), db0 = smem_desc(0, bmn);
-        const int n_kb = k_hi(P) - k_lo(P), seg = seg_blocks(n_kb);
+        const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0, seg = seg_blocks(hi - lo);
         uint32_t d = tmem + buf * buf_cols;
-        for (int kb = 0, in = 0; kb < n_kb; ++kb) {
+        int in = 0;  // k-blocks in the present segment
+        for (int kb = lo; kb < hi;) {
           if (!mbar_wait(&full[st], phase, status, kStatusTimeoutTmaFull, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(smem) + (uint32_t)(st * sbytes);
-          // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
-          const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | ((a0 + kABytes) >> 4 & 0x3FFF);
+          const int ns = min(subs, (kb < kb0 ? min(hi, kb0) : hi) - kb);  // (a stage never spans two operand pairs)
+          uint32_t a0 = smem0 + (uint32_t)(st * sbytes);
+          for (int i = 0; i < ns; ++i, ++kb, a0 += sub_bytes) {
+            // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
+            const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | ((a0 + kABytes) >> 4 & 0x3FFF);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
-            if constexpr (CG == 2)
-              tc_mma_bf16_pair(d, da + k * sa, db + k * sb, idesc, acc);
-            else
-              tc_mma_bf16(d, da + k * sa, db + k * sb, idesc, acc);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
+              if constexpr (CG == 2)
+                tc_mma_bf16_pair(d, da + k * sa, db + k * sb, idesc, acc);
+              else
+                tc_mma_bf16(d, da + k * sa, db + k * sb, idesc, acc);
+            }
+            ++in;
           }
-          if constexpr (CG == 2) {
-            tc_commit_pair(smem_u32(&empty[st]));
-            tc_commit_pair(cluster_addr(&empty[st], 1));
-          } else {
+          if constexpr (CG == 2)
+            tc_commit_both(smem_u32(&empty[st]));
+          else
             tc_commit(&empty[st]);
-          }
           if (++st == stages) st = 0, phase ^= 1;
-          if (++in == seg) in = 0, d += bn;
+          if (in >= seg) in = 0, d += bn;
         }
-        if constexpr (CG == 2) {
-          tc_commit_pair(smem_u32(&accf[buf]));
-          tc_commit_pair(cluster_addr(&accf[buf], 1));
-        } else {
+        if constexpr (CG == 2)
+          tc_commit_both(smem_u32(&accf[buf]));
+        else
           tc_commit(&accf[buf]);
-        }
         if (++buf == nbuf) buf = 0, bphase ^= 1;
       }
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     pdl_wait();
-    const int quad = warp & 3, te = threadIdx.x - 64;
+    const int quad = warp & 3, half = (warp - 2) >> 2, te = threadIdx.x - 64;
     for (int i = 0; i < g.n_sums; ++i) {
       const OpColSum cs = g.sums[i];
-      for (int c = blockIdx.x * 128 + te; c < cs.cols; c += gridDim.x * 128) {
+      for (int c = blockIdx.x * 256 + te; c < cs.cols; c += gridDim.x * 256) {
         float a = 0.f;
 #pragma unroll 16
         for (int r = 0; r < cs.rows; ++r) a += cs.part[(size_t)r * cs.cols + c];
         cs.out[c] = a;
       }
     }
-    uint8_t* stg = sStg + quad * kStg;
+    uint8_t* stg = sStg + (warp - 2) * kStg;
     int buf = 0;
     uint32_t bphase = 0;
     for (int t = unit; t < g.tiles; t += units) {
@@ -417,7 +492,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         if (mw < pM) {
           const int r = quad * 32 + lane;
           uint8_t* row = smem + (size_t)r * bn * 4;
-          for (int c = 0; c < bn; c += 32) {
+          for (int c = 32 * half; c < bn; c += 64) {
             float v[32];
             acc32(c, v);
 #pragma unroll
@@ -428,46 +503,69 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
         }
         break;  // one tile per cluster; the rest after the cluster barrier
       }
-      const int step = gated ? 32 : 64, width = gated ? bn / 2 : bn;
-      for (int c = 0; c < width; c += step) {
-        float v[32];
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          acc32(gated ? c + h * (bn / 2) : c + 32 * h, v);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(stg + stg_off(lane, 8 * h + q, gated)) =
-                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
-        if (c + step >= width) tc_fence_before();
+      // 32 output columns at a time: everything but the residual in registers
+      // (a row per lane), then through the staging
+      const int width = gated ? bn / 2 : bn;
+      auto drained = [&] {  // this warp's reads of the accumulator are done
+        tc_fence_before();
         __syncwarp();
-        if (c + step >= width && lane == 0) {  // this warp's reads of the accumulator are done
+        if (lane == 0) {
           if (CG == 2 && rank == 1)
             mbar_arrive_cluster(cluster_addr(&acce[buf], 0));
           else
             mbar_arrive(&acce[buf]);
         }
-        if (mw < pM) {
-          if (gated) {
-            if (e.vec)
-              finish_vec<true>(e, stg, lane, mw, pM, n0 + c, pN);
-            else
-              finish_any<true>(e, stg, lane, mw, pM, n0 + c, pN);
-          } else {
-            if (e.vec)
-              finish_vec<false>(e, stg, lane, mw, pM, n0 + c, pN);
-            else
-              finish_any<false>(e, stg, lane, mw, pM, n0 + c, pN);
+      };
+      if (32 * half >= width) drained();  // (a 32-column tile: nothing for the second half)
+      for (int c = 32 * half; c < width; c += 64) {
+        Window w{mw, pM, n0 + c, pN, e.ld, e.vec};
+        const bool live = mw < pM && n0 + c < pN;
+        float v[32];
+        if (gated) {
+          float u[32];
+          acc32(c, v);
+          acc32(bn / 2 + c, u);
+          if (c + 64 >= width) drained();
+          if (!live) continue;
+          add_bias(v, e.bias, w.n0, pN, e.vec);
+          add_bias(u, e.bias2, w.n0, pN, e.vec);
+          if (e.z) {
+            out_bf16(v, e.z, w, stg, lane);
+            out_bf16(u, e.z2, w, stg, lane);
           }
+          act_apply<true, 32>(e.act, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= u[j];
+          out_bf16(v, e.out, w, stg, lane);
+        } else {
+          ResidualVec<float> rf;
+          ResidualVec<__nv_bfloat16> rb;
+          if (e.res && live && e.vec) {
+            if (e.out_f32)
+              rf.load(e.res, w, lane);
+            else
+              rb.load(e.res, w, lane);
+          }
+          acc32(c, v);
+          if (c + 64 >= width) drained();
+          if (!live) continue;
+          add_bias(v, e.bias, w.n0, pN, e.vec);
+          if (e.z) out_bf16(v, e.z, w, stg, lane);
+          act_apply<true, 32>(e.act, v);
+          if (e.out_f32)
+            out_stream<float>(v, e.out, e.res, rf, w, stg, lane);
+          else if (e.res)
+            out_stream<__nv_bfloat16>(v, e.out, e.res, rb, w, stg, lane);
+          else
+            out_bf16(v, e.out, w, stg, lane);
         }
-        __syncwarp();
       }
       if (++buf == nbuf) buf = 0, bphase ^= 1;
     }
   } else if (MANUAL) {
     // ------------------------------------------------------------- loaders
     pdl_wait();
-    const int tl_ = threadIdx.x - 192;
+    const int tl_ = threadIdx.x - kThreads;
     int it = 0, s = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -526,7 +624,7 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
   if (S > 1) {  // (uniform over the cluster, reached on every path)
     __syncwarp();
     cluster_sync();  // every partial tile is in place
-    if (warp >= 2 && warp < 6 && !*abort_flag) {
+    if (warp >= 2 && warp < 2 + kEpiWarps && !*abort_flag) {
       const Tile tl = tile_at(g, unit);
       const ProductK& P = g.p[tl.p];
       const int m0 = tl.m * BM, n0 = tl.n * (P.gated ? P.bn / 2 : P.bn);
@@ -539,14 +637,14 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
       const OpEpi e = P.e;
       if (P.gated) {
         if (e.vec)
-          finish_split<false, true, 4>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, true, 4>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, true, 1>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, true, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
       } else {
         if (e.vec)
-          finish_split<false, false, 8>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, false, 8>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, false, 1>(e, P.bn, P.N, base, S, te, 128, r_lo, r_hi, m0, n0);
+          finish_split<false, false, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
       }
     }
   }
@@ -576,7 +674,8 @@ __global__ void __launch_bounds__(MANUAL ? 320 : 192, 1) op_gemm_kernel(const __
 // ------------------------------------------------------------------- host --
 struct Device {
   std::atomic<int> ready{0};
-  int sms = 148, pairs = 74;
+  int sms = 148;
+  int clusters[9];  // clusters of n CTAs (one per SM) that run at once
 };
 Device g_dev[64];
 
@@ -593,20 +692,24 @@ cudaError_t device_info(Device** out) {
         (e = cudaFuncSetAttribute(op_gemm_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(op_gemm_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess)
       return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(192);
-    cfg.dynamicSmemBytes = kSmemMax;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int pairs = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&pairs, op_gemm_kernel<2, false>, &cfg)) != cudaSuccess) return e;
+    for (int n = 1; n <= 8; ++n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(sms / n * n);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmemMax;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = n;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int c = 0;
+      e = n == 2 ? cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<2, false>, &cfg)
+                 : cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<1, false>, &cfg);
+      if (e != cudaSuccess) return e;
+      d.clusters[n] = std::max(1, std::min(c, sms / n));
+    }
     d.sms = sms;
-    d.pairs = std::max(1, std::min(pairs, sms / 2));
     d.ready.store(1, std::memory_order_release);
   }
   *out = &d;
@@ -630,34 +733,49 @@ int tile_cols(const OpProduct& p, const Plan& pl) {
 }
 int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, BK); }
 
-// Estimated clocks of a plan: the busiest CTA (pair)'s k-blocks at the
-// measured cost of one, plus the parts that nothing overlaps.
+// Estimated ns of a plan, from measured parts: one k-block of a tile (all SMs
+// busy, operands from L2), what follows a tile's last MMA, and the launch.
 double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
-  const double per = pl.cg == 2 ? (pl.bn == 256 ? 560 : 320) : pl.bn == 256 ? 580 : pl.bn == 128 ? 380 : 270;
-  const int units = pl.cg == 2 ? d.pairs : d.sms;
+  const double per = pl.cg == 2 ? (pl.bn == 256 ? 370 : 270) : pl.bn == 256 ? 410 : pl.bn == 128 ? 250 : 180;
+  const double tail = 11.0 * pl.bn + 600;
   if (pl.split > 1) {
     const OpProduct& q = p[0];
     const int bn = tile_cols(q, pl), tn = ceil_div(q.gated ? 2 * q.N : q.N, bn), tm = ceil_div(q.M, BM);
-    const int waves = ceil_div(tm * tn * pl.split, units);
-    return waves * (ceil_div(k_blocks(q), pl.split) * per + 4500.0 + 6.0 * bn);
+    const int waves = ceil_div(tm * tn, d.clusters[pl.split]);
+    return waves * (ceil_div(k_blocks(q), pl.split) * per + tail + 2500);
   }
-  double load[160];
-  for (int u = 0; u < units && u < 160; ++u) load[u] = 0;
-  long long pos = 0;
+  const int units = pl.cg == 2 ? d.clusters[2] : d.sms;
+  const bool bare = 2 * pl.seg * pl.bn > 512;  // one accumulator buffer: every tile's epilogue stands alone
+  const double extra = bare ? tail : 150;
+  if (n == 1) {
+    const int bn = tile_cols(p[0], pl), cols = p[0].gated ? 2 * p[0].N : p[0].N;
+    const long long tiles = (long long)ceil_div(p[0].M, BM * pl.cg) * ceil_div(cols, bn);
+    return (double)((tiles + units - 1) / units) * (k_blocks(p[0]) * per + extra) + tail;
+  }
+  // several products: the busiest unit's tiles
+  double worst = 0;
+  int first[kOpProducts];
+  long long whole[kOpProducts], rest[kOpProducts], pos = 0;
+  double c[kOpProducts];
   for (int i = 0; i < n; ++i) {
-    const int bn = tile_cols(p[i], pl);
-    const long long tiles = (long long)ceil_div(p[i].M, BM * pl.cg) * ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, bn);
-    const double c = k_blocks(p[i]) * per + 300;
-    const long long all = tiles / units;
-    for (int u = 0; u < units && u < 160; ++u) {
-      const int off = (int)((u - pos % units + units) % units);
-      load[u] += (all + (off < tiles % units ? 1 : 0)) * c;
-    }
+    const long long tiles = (long long)ceil_div(p[i].M, BM * pl.cg) *
+                            ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl));
+    c[i] = k_blocks(p[i]) * per + extra;
+    first[i] = (int)(pos % units);
+    whole[i] = tiles / units;
+    rest[i] = tiles % units;
     pos += tiles;
   }
-  double worst = 0;
-  for (int u = 0; u < units && u < 160; ++u) worst = std::max(worst, load[u]);
-  return worst + 2500.0 + 12.0 * pl.bn;
+  for (int u = 0; u < units; ++u) {
+    double load = 0;
+    for (int i = 0; i < n; ++i) {
+      int off = u - first[i];
+      if (off < 0) off += units;
+      load += (whole[i] + (off < rest[i])) * c[i];
+    }
+    worst = std::max(worst, load);
+  }
+  return worst + tail;
 }
 
 Plan choose(const OpProduct* p, int n, bool manual, const Device& d) {
@@ -748,19 +866,21 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int 
   }
   g.tiles = tiles;
   g.split = pl.split;
-  g.stage_bytes = kABytes + bmax / pl.cg * BK * 2;
-  g.stages = std::min(kMaxStages, (kSmemMax - kBarBytes - 4 * kStg) / g.stage_bytes);
+  g.sub_bytes = kABytes + bmax / pl.cg * BK * 2;
+  g.subs = !manual && 6 * g.sub_bytes <= kSmemMax - kBarBytes - kEpiWarps * kStg ? 2 : 1;
+  g.stage_bytes = g.subs * g.sub_bytes;
+  g.stages = std::min(kMaxStages, (kSmemMax - kBarBytes - kEpiWarps * kStg) / g.stage_bytes);
   g.nseg = pl.seg;
   g.nbuf = pl.split == 1 && 2 * pl.seg * bmax <= 512 ? 2 : 1;
   g.tm_cols = 32;
   while (g.tm_cols < g.nbuf * pl.seg * bmax) g.tm_cols *= 2;
-  const size_t smem = (size_t)g.stages * g.stage_bytes + 4 * kStg + kBarBytes;
+  const size_t smem = (size_t)g.stages * g.stage_bytes + kEpiWarps * kStg + kBarBytes;
 
   const int cluster = pl.cg == 2 ? 2 : pl.split;
-  const int units = pl.split > 1 ? tiles : std::min(tiles, pl.cg == 2 ? d->pairs : d->sms);
+  const int units = pl.split > 1 ? tiles : std::min(tiles, pl.cg == 2 ? d->clusters[2] : d->sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * cluster);
-  cfg.blockDim = dim3(manual ? 320 : 192);
+  cfg.blockDim = dim3(manual ? kThreads + kLoaders : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];

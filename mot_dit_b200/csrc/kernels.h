@@ -449,7 +449,7 @@ struct ActGrad {
   float* part;
   int M, N, ld_dz, act, f32, dy_f32, chunks;
 };
-int act_grad_chunks(int M);
+int act_grad_chunks(int M, int N, bool f32);
 // The sums alone (a call that wants no product).
 cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s);
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);

@@ -77,7 +77,7 @@ BwdLayout bwd_layout(int dtype, int M, int N, int K, int sides, bool need_dz) {
   l.dz = at;
   if (need_dz) at += sides * up((size_t)M * l.ldn * esize(dtype));
   l.part = at;
-  at += up((size_t)sides * act_grad_chunks(M) * N * 4);
+  at += up((size_t)sides * act_grad_chunks(M, N, dtype == WAM_FP32) * N * 4);
   l.x = at;
   if (dtype == WAM_BF16 && K % 8) at += up((size_t)M * l.ldk * 2);
   l.w = at;
@@ -163,6 +163,7 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
   const BwdLayout l = bwd_layout(dtype, M, N, K, 1, !as_is);
   char* ws = reinterpret_cast<char*>(workspace);
   cudaError_t err;
+  const int chunks = act_grad_chunks(M, N, dtype == WAM_FP32);
   float* part = db ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   if (db || !as_is) {
     ActGrad a{};
@@ -176,7 +177,7 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
     a.act = act;
     a.f32 = dtype == WAM_FP32;
     a.dy_f32 = dy_dtype == WAM_FP32;
-    a.chunks = act_grad_chunks(M);
+    a.chunks = chunks;
     if ((err = launch_act_grad(a, s)) != cudaSuccess) return status_of(err);
   }
   const bool pad = dtype == WAM_BF16 && K % 8;
@@ -220,7 +221,7 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
   if (dx && N >= M) add_dx();
   if (dw) add_dw();
   if (dx && N < M) add_dx();
-  const OpColSum cs{part, db, act_grad_chunks(M), N};
+  const OpColSum cs{part, db, chunks, N};
   if (n == 0) return status_of(launch_col_sum(&cs, 1, s));
   return status_of(products(dtype, p, n, &cs, db ? 1 : 0, s));
 }
@@ -293,7 +294,7 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
   char* ws = reinterpret_cast<char*>(workspace);
   char* dg = ws + l.dz;
   char* du = dg + up((size_t)M * l.ldn * e);
-  const int chunks = act_grad_chunks(M);
+  const int chunks = act_grad_chunks(M, F, dtype == WAM_FP32);
   float* part = dbias_g ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   ActGrad a{};
   a.dy = da;

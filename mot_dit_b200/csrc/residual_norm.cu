@@ -41,12 +41,14 @@ int row_threads(int D, int nv) {
 int rows_at_once(int tpr) { return tpr >= kRowThreads ? 1 : kRowThreads / tpr; }
 int elems(int D) { return D > 4096 ? 16 : 8; }
 
-// Element j of thread t: E = 8 consecutive, else strided by the row's threads.
+// Element j of thread t: groups of E consecutive elements, a row's threads
+// side by side.
 template <int E>
 __device__ __forceinline__ int elem(int t, int tpr, int j) {
-  return E == 8 ? (t + (j / 8) * tpr) * 8 + j % 8 : t + j * tpr;
+  return (t + (j / E) * tpr) * E + j % E;
 }
 // A row's elements of this thread, unconverted (zero past the row's end).
+// E = 8: 16-byte accesses.
 template <int E, int NV, typename T>
 struct Row {
   Raw<T, E> r[NV / E];
@@ -64,19 +66,135 @@ struct Row {
 #pragma unroll
     for (int k = 0; k < NV / E; ++k) r[k].zero();
   }
-  __device__ __forceinline__ void get(float (&v)[NV]) const {
+  __device__ __forceinline__ void get(float (&v)[NV], int, int, int) const {
 #pragma unroll
     for (int k = 0; k < NV / E; ++k) r[k].get(v + E * k);
   }
 };
-template <int E, int NV, typename T>
-__device__ __forceinline__ void row_store(T* p, int D, int t, int tpr, const float (&v)[NV]) {
+// E = 2, any alignment.  fp32: single words.
+template <int NV>
+struct Row<2, NV, float> {
+  float v_[NV];
+  __device__ __forceinline__ void load(const float* p, int D, int t, int tpr) {
 #pragma unroll
-  for (int k = 0; k < NV / E; ++k) {
-    const int i = elem<E>(t, tpr, E * k);
-    if (i < D) store_to<E>(p + i, v + E * k);
+    for (int j = 0; j < NV; ++j) {
+      const int i = elem<2>(t, tpr, j);
+      v_[j] = i < D ? p[i] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v_[j] = 0.f;
+  }
+  __device__ __forceinline__ void get(float (&v)[NV], int, int, int) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = v_[j];
+  }
+};
+// bf16 pairs (2 k, 2 k + 1), in 4-byte words whatever the row's alignment.  A
+// row that starts on a word holds its pairs in one word each.  One that
+// starts two bytes past a word (`odd`) has pair k in the words k (its upper
+// half) and k + 1 (its lower half): a thread loads word k and takes the next
+// thread's from the neighbouring lane; where there is none (the last lane of
+// the warp or of the row, the row's last word) the element is loaded by
+// itself, and so is element 0 (word 0 reaches back before the row).
+template <int NV>
+struct Row<2, NV, __nv_bfloat16> {
+  uint32_t w[NV / 2];
+  unsigned short x[NV / 2];
+  bool odd;
+  __device__ __forceinline__ static bool edge(int t, int tpr, int k, int D) {
+    return (threadIdx.x + threadIdx.y * blockDim.x) % 32 == 31 || t == tpr - 1 || 2 * k + 2 >= D;
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int D, int t, int tpr) {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+    odd = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+    if (!odd) {
+#pragma unroll
+      for (int j = 0; j < NV / 2; ++j) {
+        const int i = 2 * (t + j * tpr);
+        w[j] = 0;
+        if (i + 1 < D)
+          w[j] = *reinterpret_cast<const uint32_t*>(q + i);
+        else if (i < D)
+          w[j] = q[i];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV / 2; ++j) {
+        const int k = t + j * tpr, i = 2 * k;
+        w[j] = 0;
+        x[j] = 0;
+        if (i < D) {
+          if (k == 0)
+            w[j] = (uint32_t)q[0] << 16;
+          else
+            w[j] = *reinterpret_cast<const uint32_t*>(q + i - 1);
+          if (i + 1 < D && edge(t, tpr, k, D)) x[j] = q[i + 1];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+    odd = false;
+#pragma unroll
+    for (int j = 0; j < NV / 2; ++j) w[j] = 0, x[j] = 0;
+  }
+  // (every lane of the warp takes part: rows of one warp may differ in `odd`)
+  __device__ __forceinline__ void get(float (&v)[NV], int t, int tpr, int D) const {
+#pragma unroll
+    for (int j = 0; j < NV / 2; ++j) {
+      const uint32_t next = __shfl_down_sync(0xffffffffu, w[j], 1);
+      const uint32_t hi = edge(t, tpr, t + j * tpr, D) ? (uint32_t)x[j] << 16 : next << 16;
+      v[2 * j] = __uint_as_float(odd ? w[j] & 0xffff0000u : w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(odd ? hi : w[j] & 0xffff0000u);
+    }
+  }
+};
+// Stores the row if it is live (every lane takes part).
+template <int E, int NV, typename T>
+__device__ __forceinline__ void row_store(T* p, bool live, int D, int t, int tpr, const float (&v)[NV]) {
+  if constexpr (E == 8) {
+    if (!live) return;
+#pragma unroll
+    for (int k = 0; k < NV / E; ++k) {
+      const int i = elem<E>(t, tpr, E * k);
+      if (i < D) store_to<E>(p + i, v + E * k);
+    }
+  } else if constexpr (sizeof(T) == 4) {
+    if (!live) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = elem<2>(t, tpr, j);
+      if (i < D) p[i] = v[j];
+    }
+  } else {
+    // A row two bytes past a word: its word k joins the pair below (from the
+    // lane before) and mine; the halves at a warp's or the row's ends alone.
+    unsigned short* q = reinterpret_cast<unsigned short*>(p);
+    const bool odd = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+#pragma unroll
+    for (int j = 0; j < NV / 2; ++j) {
+      const int k = t + j * tpr, i = 2 * k;
+      const uint32_t w = pack_bf16(v[2 * j], v[2 * j + 1]);
+      const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1);
+      if (!live || i >= D) continue;
+      if (!odd) {
+        if (i + 1 < D)
+          *reinterpret_cast<uint32_t*>(q + i) = w;
+        else
+          q[i] = (unsigned short)w;
+      } else {
+        if ((threadIdx.x + threadIdx.y * blockDim.x) % 32 == 0 || t == 0)
+          q[i] = (unsigned short)w;
+        else
+          *reinterpret_cast<uint32_t*>(q + i - 1) = before >> 16 | w << 16;
+        if (i + 1 < D && Row<2, NV, T>::edge(t, tpr, k, D)) q[i + 1] = (unsigned short)(w >> 16);
+      }
+    }
   }
 }
+
 // A column vector's elements of this thread (fill without one).
 template <int E, int NV>
 __device__ __forceinline__ void vec_load(const float* p, float fill, int D, int t, int tpr, float (&v)[NV]) {
@@ -88,7 +206,7 @@ __device__ __forceinline__ void vec_load(const float* p, float fill, int D, int 
   if (E == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
     Row<8, NV, float> r;
     r.load(p, D, t, tpr);
-    r.get(v);
+    r.get(v, t, tpr, D);
     return;
   }
 #pragma unroll
@@ -98,27 +216,54 @@ __device__ __forceinline__ void vec_load(const float* p, float fill, int D, int 
   }
 }
 
-// Sums of K values over the threads of each row.  One barrier; `sh` holds
-// [2][rows][K][32], the halves taken in turn.
+// Sums of K (1 or 6) values over the threads of each row.  Within a warp the
+// six are reduced together: each exchange halves what a lane carries (8, 4, 2,
+// 1 values), so that it takes 9 shuffles and not 30.  Across warps: one
+// barrier; `sh` holds [2][rows][warps][8], the halves taken in turn.
 template <int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, int rows, float* sh, int& phase) {
-  const int w = tpr < 32 ? tpr : 32;
+  constexpr unsigned all = 0xffffffffu;
+  if (tpr <= 32) {
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-    for (int o = w / 2; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (tpr > 32) {
-    float* b = sh + (phase * rows + ry) * K * 32;
-    phase ^= 1;
-    if ((t & 31) == 0)
+    for (int k = 0; k < K; ++k)
+      for (int o = tpr / 2; o > 0; o >>= 1) v[k] += __shfl_xor_sync(all, v[k], o);
+    return;
+  }
+  const int lane = t & 31, warp = t >> 5, warps = tpr >> 5;
+  float* b = sh + (phase * rows + ry) * warps * 8;
+  phase ^= 1;
+  if constexpr (K == 1) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) b[k * 32 + (t >> 5)] = v[k];
+    for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(all, v[0], o);
+    if (lane == 0) b[warp * 8] = v[0];
     __syncthreads();
+    float a = 0.f;
+    for (int i = 0; i < warps; ++i) a += b[i * 8];
+    v[0] = a;
+  } else {
+    static_assert(K == 6, "1 or 6 values");
+    float x[4], y[2], z;
+    const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float a = 0.f;
-      for (int i = 0; i < tpr / 32; ++i) a += b[k * 32 + i];
-      v[k] = a;
+    for (int k = 0; k < 4; ++k) {  // lanes 16..31 keep values 4..7 (6, 7: none)
+      const float lo = v[k], hi = k < 2 ? v[4 + k] : 0.f;
+      x[k] = (h16 ? hi : lo) + __shfl_xor_sync(all, h16 ? lo : hi, 16);
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) y[k] = (h8 ? x[2 + k] : x[k]) + __shfl_xor_sync(all, h8 ? x[k] : x[2 + k], 8);
+    z = (h4 ? y[1] : y[0]) + __shfl_xor_sync(all, h4 ? y[0] : y[1], 4);
+    z += __shfl_xor_sync(all, z, 2);
+    z += __shfl_xor_sync(all, z, 1);
+    if ((lane & 3) == 0) b[warp * 8 + (lane >> 2)] = z;  // lane bits 4, 3, 2 = the value's number
+    __syncthreads();
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < warps; ++i) {
+      const float4 p = *reinterpret_cast<const float4*>(b + i * 8);
+      const float2 q = *reinterpret_cast<const float2*>(b + i * 8 + 4);
+      s[0] += p.x, s[1] += p.y, s[2] += p.z, s[3] += p.w, s[4] += q.x, s[5] += q.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 6; ++k) v[k] = s[k];
   }
 }
 
@@ -144,7 +289,7 @@ __device__ __forceinline__ void coef(const ResNorm& a, int grp, int t, int tpr, 
 // the stream's and the compute type.
 template <int E, int NV, typename RT, typename CT>
 __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
-  __shared__ float sh[2 * 8 * 32];  // (rows > 8 only when a row is within a warp)
+  __shared__ __align__(16) float sh[2 * 16 * 8];  // [2][rows][warps][8]: at most 16 warps in all
   const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y, D = a.D;
   const int lo = (int)((long long)a.M * blockIdx.x / gridDim.x), hi = (int)((long long)a.M * (blockIdx.x + 1) / gridDim.x);
   const RT* px = reinterpret_cast<const RT*>(a.x);
@@ -171,8 +316,8 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
     if (gr != grp) coef<E, NV>(a, gr, t, tpr, mul, add, w);
     grp = gr;
     float v[NV], q[NV];
-    rx.get(v);
-    ryy.get(q);
+    rx.get(v, t, tpr, D);
+    ryy.get(q, t, tpr, D);
     load(m + R);
     float s1[1] = {0.f};
     float rp = 1.f;
@@ -190,12 +335,10 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
     }
     row_sum<1>(s1, t, tpr, ry, R, sh, phase);
     const float r = 1.f / sqrtf(s1[0] / (float)D + kEps);
-    if (live) {
-      row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, D, t, tpr, v);
+    row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, live, D, t, tpr, v);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
-      row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, D, t, tpr, v);
-    }
+    for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
+    row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, live, D, t, tpr, v);
   }
 }
 
@@ -204,7 +347,7 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
 template <int E, int NV, bool AHEAD, typename RT, typename CT>
 __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a, int chunks) {
   extern __shared__ float dyn[];    // [rows][3][tpr NV] column sums of the row lanes (rows > 1)
-  __shared__ float sh[2 * 6 * 8 * 32];
+  __shared__ __align__(16) float sh[2 * 16 * 8];
   const ResNorm& f = a.f;
   const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y, D = f.D;
   const int grp = blockIdx.x / chunks, ck = blockIdx.x % chunks, g_lo = grp * f.rows_per_group, g_n = min(f.rows_per_group, f.M - g_lo);
@@ -241,7 +384,7 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
     const bool live = m < hi;
     if (!AHEAD) load(m);
     float s[NV], y[NV], ds[NV], dh[NV];
-    xs.get(s), xy.get(y), xd.get(ds), xh.get(dh);
+    xs.get(s, t, tpr, D), xy.get(y, t, tpr, D), xd.get(ds, t, tpr, D), xh.get(dh, t, tpr, D);
     if (AHEAD) load(m + R);
     float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -272,10 +415,8 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
       ds[j] = f.alpha * dv;
       dh[j] = f.post ? rp * (dv * w[j] - y[j] * cy) : dv * w[j];
     }
-    if (live) {
-      row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, ds);
-      row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, dh);
-    }
+    row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, live, D, t, tpr, ds);
+    row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, live, D, t, tpr, dh);
   }
   if (!a.part) return;
   float* part = a.part + (size_t)blockIdx.x * 3 * D;
@@ -410,9 +551,9 @@ cudaError_t by_form(bool vec, int D, bool res_f32, bool f32, F f) {
   using std::integral_constant;
   if (elems(D) == 8)
     return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 8>{})
-               : types(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+               : types(integral_constant<int, 2>{}, integral_constant<int, 8>{});
   return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 16>{})
-             : types(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+             : types(integral_constant<int, 2>{}, integral_constant<int, 16>{});
 }
 
 }  // namespace
