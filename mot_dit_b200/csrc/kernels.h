@@ -494,6 +494,7 @@ size_t res_norm_part_floats(int M, int D, int rows_per_group);
 cudaError_t launch_res_norm_grad(const ResNormGrad& a, cudaStream_t s);
 // Bits of the bounded waits that gave up on the current device, and clears them (synchronous).
 cudaError_t op_gemm_status(unsigned* bits);
+cudaError_t res_norm_status(unsigned* bits);  // (after a synchronisation)
 
 // TMA tensor-map creation (driver entry point resolved at run time).
 bool make_tmap_3d(CUtensorMap* map, const void* base, int K, int rows, int nmat, size_t mat_stride_bytes,

@@ -95,9 +95,9 @@ bool direct(int dtype, int N, int act, int dy_dtype) {
 extern "C" {
 
 wam_status wam_ops_check_status(void) {
-  unsigned bits = 0;
-  if (op_gemm_status(&bits) != cudaSuccess) return WAM_ERR_CUDA;
-  return bits ? WAM_ERR_TIMEOUT : WAM_OK;
+  unsigned gemm = 0, norm = 0;
+  if (op_gemm_status(&gemm) != cudaSuccess || res_norm_status(&norm) != cudaSuccess) return WAM_ERR_CUDA;
+  return gemm | norm ? WAM_ERR_TIMEOUT : WAM_OK;
 }
 
 // ------------------------------------------------------------------ linear --

@@ -7,19 +7,22 @@
 // and the parameter gradients are column sums of dh n, dh and dv q.
 //
 // Bound by memory: forward 4, backward 6 row passes, each element read or
-// written once.  Eight elements of a row sit in one thread's registers (a row
-// is shared by D / 8 threads of a block, narrow rows by part of a warp), the
-// column vectors of the block's sample stay there too, and the next row is
-// requested before the present one is reduced.  The backward pass needs the
-// mean of dp post_gain q, which depends on dv and so on the first means; it is
-// expanded by linearity into three more sums of the same round, so that a row
-// costs one block barrier: sum dv w y = sum w y ds + r sum w y dn - r^3 mean(dn s)
-// sum w y s, w = gate post_gain.  Column sums stay in registers over a block's
-// rows (all of one sample), go to a partial array once, and a second kernel
-// adds the partials in order: no atomics, the same bits every time.
+// written once.  A producer warp keeps a ring of row groups filled with
+// asynchronous bulk copies (rows are contiguous, so a group is one span per
+// matrix, widened to 16-byte granules: the ring takes any row length and
+// alignment, and costs the row threads no registers).  A row's threads hold
+// NV columns each; the column vectors of the block's sample stay in their
+// registers.  The backward pass needs the mean of dp post_gain q, which depends
+// on dv and so on the first means; it is expanded by linearity into three more
+// sums of the same round, so that a row costs one block barrier: sum dv w y =
+// sum w y ds + r sum w y dn - r^3 mean(dn s) sum w y s, w = gate post_gain.
+// Column sums stay in registers over a block's rows (all of one sample), go to
+// a partial array once, and a second kernel adds the partials in order: no
+// atomics, the same bits every time.
 #include <algorithm>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "kernels.h"
 #include "op_epilogue.cuh"
 
@@ -27,7 +30,12 @@ namespace wam {
 namespace {
 
 constexpr float kEps = 1e-6f;
-constexpr int kRowThreads = 256;  // threads of a block when a row needs fewer
+constexpr int kRowThreads = 224;  // row threads of a block when a row needs fewer (256 with the producer)
+constexpr int kMaxStages = 8;
+constexpr int kRing = 56 * 1024;      // ring of a block (several blocks an SM) ...
+constexpr int kRingWide = 200 * 1024; // ... when two stages fit it, else this
+
+__device__ unsigned g_norm_status;
 
 // Threads that share a row: NV elements each; a power of two below a warp,
 // whole warps above.
@@ -39,189 +47,78 @@ int row_threads(int D, int nv) {
   return p;
 }
 int rows_at_once(int tpr) { return tpr >= kRowThreads ? 1 : kRowThreads / tpr; }
-int elems(int D) { return D > 4096 ? 16 : 8; }
+int elems(int D) { return D > 3840 ? 24 : 8; }  // (blocks of at most 512 / 384 threads)
+
+// The ring's shape: `rows` rows of up to four matrices a stage.
+struct Ring {
+  int stages, stage_bytes;
+  int off[4];  // of each matrix in a stage
+};
+Ring ring_of(int D, int rows, std::initializer_list<int> sizes) {
+  Ring r{};
+  int at = 0, i = 0;
+  for (int e : sizes) {
+    r.off[i++] = at;
+    at += (rows * D * e + 15) / 16 * 16 + 16;  // (a span that starts inside a granule takes one more)
+  }
+  r.stage_bytes = (at + 127) / 128 * 128;
+  const int budget = 2 * r.stage_bytes <= kRing ? kRing : kRingWide;
+  r.stages = std::max(1, std::min(kMaxStages, budget / r.stage_bytes));
+  return r;
+}
 
 // Element j of thread t: groups of E consecutive elements, a row's threads
-// side by side.
+// side by side (E = 8 where 16-byte accesses may be used, else 1).
 template <int E>
 __device__ __forceinline__ int elem(int t, int tpr, int j) {
   return (t + (j / E) * tpr) * E + j % E;
 }
-// A row's elements of this thread, unconverted (zero past the row's end).
-// E = 8: 16-byte accesses.
+// This thread's elements of a row in shared memory (zero past its end).
 template <int E, int NV, typename T>
-struct Row {
-  Raw<T, E> r[NV / E];
-  __device__ __forceinline__ void load(const T* p, int D, int t, int tpr) {
+__device__ __forceinline__ void row_get(const T* p, int D, int t, int tpr, float (&v)[NV]) {
 #pragma unroll
-    for (int k = 0; k < NV / E; ++k) {
-      const int i = elem<E>(t, tpr, E * k);
-      if (i < D)
-        r[k].load(p + i);
-      else
-        r[k].zero();
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int k = 0; k < NV / E; ++k) r[k].zero();
-  }
-  __device__ __forceinline__ void get(float (&v)[NV], int, int, int) const {
-#pragma unroll
-    for (int k = 0; k < NV / E; ++k) r[k].get(v + E * k);
-  }
-};
-// E = 2, any alignment.  fp32: single words.
-template <int NV>
-struct Row<2, NV, float> {
-  float v_[NV];
-  __device__ __forceinline__ void load(const float* p, int D, int t, int tpr) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = elem<2>(t, tpr, j);
-      v_[j] = i < D ? p[i] : 0.f;
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v_[j] = 0.f;
-  }
-  __device__ __forceinline__ void get(float (&v)[NV], int, int, int) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = v_[j];
-  }
-};
-// bf16 pairs (2 k, 2 k + 1), in 4-byte words whatever the row's alignment.  A
-// row that starts on a word holds its pairs in one word each.  One that
-// starts two bytes past a word (`odd`) has pair k in the words k (its upper
-// half) and k + 1 (its lower half): a thread loads word k and takes the next
-// thread's from the neighbouring lane; where there is none (the last lane of
-// the warp or of the row, the row's last word) the element is loaded by
-// itself, and so is element 0 (word 0 reaches back before the row).
-template <int NV>
-struct Row<2, NV, __nv_bfloat16> {
-  uint32_t w[NV / 2];
-  unsigned short x[NV / 2];
-  bool odd;
-  __device__ __forceinline__ static bool edge(int t, int tpr, int k, int D) {
-    return (threadIdx.x + threadIdx.y * blockDim.x) % 32 == 31 || t == tpr - 1 || 2 * k + 2 >= D;
-  }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int D, int t, int tpr) {
-    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-    odd = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
-    if (!odd) {
-#pragma unroll
-      for (int j = 0; j < NV / 2; ++j) {
-        const int i = 2 * (t + j * tpr);
-        w[j] = 0;
-        if (i + 1 < D)
-          w[j] = *reinterpret_cast<const uint32_t*>(q + i);
-        else if (i < D)
-          w[j] = q[i];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV / 2; ++j) {
-        const int k = t + j * tpr, i = 2 * k;
-        w[j] = 0;
-        x[j] = 0;
-        if (i < D) {
-          if (k == 0)
-            w[j] = (uint32_t)q[0] << 16;
-          else
-            w[j] = *reinterpret_cast<const uint32_t*>(q + i - 1);
-          if (i + 1 < D && edge(t, tpr, k, D)) x[j] = q[i + 1];
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void zero() {
-    odd = false;
-#pragma unroll
-    for (int j = 0; j < NV / 2; ++j) w[j] = 0, x[j] = 0;
-  }
-  // (every lane of the warp takes part: rows of one warp may differ in `odd`)
-  __device__ __forceinline__ void get(float (&v)[NV], int t, int tpr, int D) const {
-#pragma unroll
-    for (int j = 0; j < NV / 2; ++j) {
-      const uint32_t next = __shfl_down_sync(0xffffffffu, w[j], 1);
-      const uint32_t hi = edge(t, tpr, t + j * tpr, D) ? (uint32_t)x[j] << 16 : next << 16;
-      v[2 * j] = __uint_as_float(odd ? w[j] & 0xffff0000u : w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(odd ? hi : w[j] & 0xffff0000u);
-    }
-  }
-};
-// Stores the row if it is live (every lane takes part).
-template <int E, int NV, typename T>
-__device__ __forceinline__ void row_store(T* p, bool live, int D, int t, int tpr, const float (&v)[NV]) {
-  if constexpr (E == 8) {
-    if (!live) return;
-#pragma unroll
-    for (int k = 0; k < NV / E; ++k) {
-      const int i = elem<E>(t, tpr, E * k);
-      if (i < D) store_to<E>(p + i, v + E * k);
-    }
-  } else if constexpr (sizeof(T) == 4) {
-    if (!live) return;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = elem<2>(t, tpr, j);
-      if (i < D) p[i] = v[j];
-    }
-  } else {
-    // A row two bytes past a word: its word k joins the pair below (from the
-    // lane before) and mine; the halves at a warp's or the row's ends alone.
-    unsigned short* q = reinterpret_cast<unsigned short*>(p);
-    const bool odd = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
-#pragma unroll
-    for (int j = 0; j < NV / 2; ++j) {
-      const int k = t + j * tpr, i = 2 * k;
-      const uint32_t w = pack_bf16(v[2 * j], v[2 * j + 1]);
-      const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1);
-      if (!live || i >= D) continue;
-      if (!odd) {
-        if (i + 1 < D)
-          *reinterpret_cast<uint32_t*>(q + i) = w;
-        else
-          q[i] = (unsigned short)w;
-      } else {
-        if ((threadIdx.x + threadIdx.y * blockDim.x) % 32 == 0 || t == 0)
-          q[i] = (unsigned short)w;
-        else
-          *reinterpret_cast<uint32_t*>(q + i - 1) = before >> 16 | w << 16;
-        if (i + 1 < D && Row<2, NV, T>::edge(t, tpr, k, D)) q[i + 1] = (unsigned short)(w >> 16);
-      }
-    }
+  for (int k = 0; k < NV / E; ++k) {
+    const int i = elem<E>(t, tpr, E * k);
+    Raw<T, E> r;
+    r.zero();
+    if (i < D) r.load(p + i);
+    r.get(v + E * k);
   }
 }
-
+template <int E, int NV, typename T>
+__device__ __forceinline__ void row_store(T* p, int D, int t, int tpr, const float (&v)[NV]) {
+#pragma unroll
+  for (int k = 0; k < NV / E; ++k) {
+    const int i = elem<E>(t, tpr, E * k);
+    if (i < D) store_to<E>(p + i, v + E * k);
+  }
+}
 // A column vector's elements of this thread (fill without one).
 template <int E, int NV>
 __device__ __forceinline__ void vec_load(const float* p, float fill, int D, int t, int tpr, float (&v)[NV]) {
   if (!p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) v[j] = fill;
-    return;
-  }
-  if (E == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    Row<8, NV, float> r;
-    r.load(p, D, t, tpr);
-    r.get(v, t, tpr, D);
-    return;
-  }
+  } else if (E == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    row_get<E, NV>(p, D, t, tpr, v);
+  } else {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = elem<E>(t, tpr, j);
-    v[j] = i < D ? p[i] : 0.f;
+    for (int j = 0; j < NV; ++j) {
+      const int i = elem<E>(t, tpr, j);
+      v[j] = i < D ? p[i] : 0.f;
+    }
   }
 }
+
+// Barrier of the block's n row threads (the producer warp is not among them).
+__device__ __forceinline__ void row_bar(int n) { asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory"); }
 
 // Sums of K (1 or 6) values over the threads of each row.  Within a warp the
 // six are reduced together: each exchange halves what a lane carries (8, 4, 2,
 // 1 values), so that it takes 9 shuffles and not 30.  Across warps: one
-// barrier; `sh` holds [2][rows][warps][8], the halves taken in turn.
+// barrier of the n row threads; `sh` holds [2][rows][warps][8], the halves taken in turn.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, int rows, float* sh, int& phase) {
+__device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, int rows, float* sh, int& phase, int n) {
   constexpr unsigned all = 0xffffffffu;
   if (tpr <= 32) {
 #pragma unroll
@@ -236,7 +133,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, i
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(all, v[0], o);
     if (lane == 0) b[warp * 8] = v[0];
-    __syncthreads();
+    row_bar(n);
     float a = 0.f;
     for (int i = 0; i < warps; ++i) a += b[i * 8];
     v[0] = a;
@@ -255,7 +152,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, i
     z += __shfl_xor_sync(all, z, 2);
     z += __shfl_xor_sync(all, z, 1);
     if ((lane & 3) == 0) b[warp * 8 + (lane >> 2)] = z;  // lane bits 4, 3, 2 = the value's number
-    __syncthreads();
+    row_bar(n);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < warps; ++i) {
       const float4 p = *reinterpret_cast<const float4*>(b + i * 8);
@@ -273,59 +170,158 @@ template <int E, int NV>
 __device__ __forceinline__ void coef(const ResNorm& a, int grp, int t, int tpr, float (&mul)[NV], float (&add)[NV],
                                      float (&w)[NV]) {
   const size_t o = (size_t)grp * a.ld_mod;
-  float x[NV];
+  float x[NV], y[NV];
   vec_load<E, NV>(a.gain, 1.f, a.D, t, tpr, mul);
   vec_load<E, NV>(a.scale ? a.scale + o : nullptr, 0.f, a.D, t, tpr, x);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) mul[j] *= 1.f + x[j];
   vec_load<E, NV>(a.shift ? a.shift + o : nullptr, 0.f, a.D, t, tpr, add);
   vec_load<E, NV>(a.gate ? a.gate + o : nullptr, 1.f, a.D, t, tpr, w);
-  vec_load<E, NV>(a.post ? a.post_gain : nullptr, 1.f, a.D, t, tpr, x);
+  vec_load<E, NV>(a.post ? a.post_gain : nullptr, 1.f, a.D, t, tpr, y);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) w[j] *= x[j];
+  for (int j = 0; j < NV; ++j) {
+    mul[j] *= 1.f + x[j];
+    w[j] *= y[j];
+  }
 }
 
-// Block: (tpr, rows); its rows are [M b / grid, M (b + 1) / grid).  RT / CT:
-// the stream's and the compute type.
-template <int E, int NV, typename RT, typename CT>
-__global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
+// ------------------------------------------------------------- the ring ----
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int abort;
+};
+__device__ __forceinline__ void bars_init(Bars& b, int stages, int warps) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&b.full[s], 1);
+      mbar_init(&b.empty[s], warps);
+    }
+    b.abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+}
+// Bytes [off, off + len) of a buffer of `total` bytes, as the 16-byte granules
+// that hold them.  A granule that reaches past either end of the buffer is
+// not read: its elements are copied one by one (`head` / `tail`).
+struct Span {
+  uintptr_t lo, hi;           // granules for the bulk copy
+  uintptr_t head, head_end;   // bytes to copy singly
+  uintptr_t tail, tail_end;
+  uintptr_t at;               // the granule that lands at the stage's start
+};
+__device__ __forceinline__ Span span_of(const void* base, size_t total, size_t off, uint32_t len) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(base), a = b + off, e = a + len;
+  Span s;
+  s.at = s.lo = a & ~(uintptr_t)15;
+  s.hi = (e + 15) & ~(uintptr_t)15;
+  s.head = s.head_end = s.tail = s.tail_end = 0;
+  if (s.lo < b) {
+    s.lo += 16;
+    s.head = a;
+    s.head_end = s.lo < e ? s.lo : e;
+  }
+  if (s.hi > b + total && s.hi > s.lo) {
+    s.hi -= 16;
+    s.tail = s.hi > a ? s.hi : a;
+    s.tail_end = e;
+  }
+  if (s.hi < s.lo) s.hi = s.lo;
+  return s;
+}
+__device__ __forceinline__ void copy_ends(uint8_t* dst, const Span& s) {
+  for (uintptr_t q = s.head; q < s.head_end; q += 2)
+    *reinterpret_cast<unsigned short*>(dst + (q - s.at)) = *reinterpret_cast<const unsigned short*>(q);
+  for (uintptr_t q = s.tail; q < s.tail_end; q += 2)
+    *reinterpret_cast<unsigned short*>(dst + (q - s.at)) = *reinterpret_cast<const unsigned short*>(q);
+}
+// The producer warp: rows [lo, hi) of N matrices, R at a time; lane i deals
+// with matrix i (one lane alone, with its 64-bit addresses, took longer than
+// the rows' arithmetic).
+template <int N>
+__device__ __forceinline__ void produce(const void* base, int size, const Ring& ring, int M, int D, int lo, int hi, int R,
+                                        uint8_t* smem, Bars& b) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < N && base;
+  uint8_t* dst = smem + ring.off[lane < N ? lane : 0];
+  const size_t total = (size_t)M * D * size, row = (size_t)D * size;
+  int st = 0, it = 0;
+  uint32_t phase = 0;
+  for (int m = lo; m < hi; m += R, ++it) {
+    if (it >= ring.stages && !__all_sync(0xffffffffu, mbar_wait(&b.empty[st], phase ^ 1, &g_norm_status,
+                                                                kStatusTimeoutTmaEmpty, (volatile int*)&b.abort)))
+      break;
+    uint8_t* d = dst + (size_t)st * ring.stage_bytes;
+    Span s{};
+    if (mine) {
+      s = span_of(base, total, m * row, (uint32_t)(min(R, hi - m) * row));
+      copy_ends(d, s);
+    }
+    uint32_t bytes = (uint32_t)(s.hi - s.lo);
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
+    __syncwarp();  // every lane's single elements are in place before the arrival that publishes them
+    if (lane == 0) mbar_arrive_expect_tx(&b.full[st], bytes);
+    __syncwarp();
+    if (mine && s.hi > s.lo) bulk_load(d + (s.lo - s.at), reinterpret_cast<const void*>(s.lo), (uint32_t)(s.hi - s.lo), &b.full[st]);
+    if (++st == ring.stages) st = 0, phase ^= 1;
+  }
+  // never leave with copies in flight
+  if (lane == 0)
+    for (int i = max(0, it - ring.stages); i < it; ++i)
+      mbar_wait(&b.full[i % ring.stages], (i / ring.stages) & 1, &g_norm_status, kStatusTimeoutDrain, nullptr);
+}
+// Row `ry` of the group that starts at row m, in a stage.
+template <typename T>
+__device__ __forceinline__ const T* staged(const uint8_t* stage, int off, const void* base, int m, int D, int ry) {
+  const uint32_t in = (uint32_t)((reinterpret_cast<uintptr_t>(base) + (size_t)m * D * sizeof(T)) & 15);
+  return reinterpret_cast<const T*>(stage + off + in) + (size_t)ry * D;
+}
+
+// Block: n = tpr x R row threads and a producer warp; its rows are
+// [M b / grid, M (b + 1) / grid).  RT / CT: the stream's and the compute type.
+template <int E, int NV, bool SMALL, typename RT, typename CT>
+__global__ void __launch_bounds__(SMALL ? 256 : NV == 8 ? 512 : 384, SMALL ? (E == 8 ? 3 : 2) : 1) res_norm_kernel(const ResNorm a, const Ring ring, int tpr, int R) {
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float sh[2 * 16 * 8];  // [2][rows][warps][8]: at most 16 warps in all
-  const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y, D = a.D;
+  __shared__ Bars bars;
+  const int n = tpr * R, D = a.D;
   const int lo = (int)((long long)a.M * blockIdx.x / gridDim.x), hi = (int)((long long)a.M * (blockIdx.x + 1) / gridDim.x);
-  const RT* px = reinterpret_cast<const RT*>(a.x);
-  const CT* py = reinterpret_cast<const CT*>(a.y);
+  bars_init(bars, ring.stages, n / 32);
   pdl_trigger();
   pdl_wait();
-  int phase = 0, grp = -1;
+  if ((int)threadIdx.x >= n) {
+    const bool first = threadIdx.x % 32 == 0;
+    produce<2>(first ? a.x : a.y, first ? sizeof(RT) : sizeof(CT), ring, a.M, D, lo, hi, R, smem, bars);
+    return;
+  }
+  const int ry = threadIdx.x / tpr, t = threadIdx.x - ry * tpr;
+  int phase = 0, st = 0, next = lo + ry;  // (next: first row that needs other coefficients)
+  uint32_t full_phase = 0;
+  const float inv = 1.f / (float)D;
   float mul[NV], add[NV], w[NV];
-  Row<E, NV, RT> rx;
-  Row<E, NV, CT> ryy;
-  auto load = [&](int m) {
-    if (m < hi) {
-      rx.load(px + (size_t)m * D, D, t, tpr);
-      ryy.load(py + (size_t)m * D, D, t, tpr);
-    }
-  };
-  rx.zero();
-  ryy.zero();
-  load(lo + ry);
   for (int m0 = lo; m0 < hi; m0 += R) {
     const int m = m0 + ry;
     const bool live = m < hi;  // (dead row lanes keep the barriers company)
-    const int gr = (live ? m : hi - 1) / a.rows_per_group;
-    if (gr != grp) coef<E, NV>(a, gr, t, tpr, mul, add, w);
-    grp = gr;
+    if (live && m >= next) {
+      const int g = m / a.rows_per_group;
+      coef<E, NV>(a, g, t, tpr, mul, add, w);
+      next = (g + 1) * a.rows_per_group;
+    }
+    // (a wait that gives up is reported; the rows go on, so that every barrier is met)
+    mbar_wait(&bars.full[st], full_phase, &g_norm_status, kStatusTimeoutTmaFull, (volatile int*)&bars.abort);
+    const uint8_t* stage = smem + (size_t)st * ring.stage_bytes;
     float v[NV], q[NV];
-    rx.get(v, t, tpr, D);
-    ryy.get(q, t, tpr, D);
-    load(m + R);
+    row_get<E, NV>(staged<RT>(stage, ring.off[0], a.x, m0, D, ry), live ? D : 0, t, tpr, v);
+    row_get<E, NV>(staged<CT>(stage, ring.off[1], a.y, m0, D, ry), live ? D : 0, t, tpr, q);
+    __syncwarp();
+    if ((t & 31) == 0 && (threadIdx.x & 31) == 0) mbar_arrive(&bars.empty[st]);
+    if (++st == ring.stages) st = 0, full_phase ^= 1;
     float s1[1] = {0.f};
     float rp = 1.f;
     if (a.post) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) s1[0] += q[j] * q[j];
-      row_sum<1>(s1, t, tpr, ry, R, sh, phase);
-      rp = 1.f / sqrtf(s1[0] / (float)D + kEps);
+      row_sum<1>(s1, t, tpr, ry, R, sh, phase, n);
+      rp = rsqrtf(s1[0] * inv + kEps);
     }
     s1[0] = 0.f;
 #pragma unroll
@@ -333,28 +329,44 @@ __global__ void __launch_bounds__(512) res_norm_kernel(const ResNorm a) {
       v[j] = a.alpha * v[j] + w[j] * (q[j] * rp);
       s1[0] += v[j] * v[j];
     }
-    row_sum<1>(s1, t, tpr, ry, R, sh, phase);
-    const float r = 1.f / sqrtf(s1[0] / (float)D + kEps);
-    row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, live, D, t, tpr, v);
+    row_sum<1>(s1, t, tpr, ry, R, sh, phase, n);
+    const float r = rsqrtf(s1[0] * inv + kEps);
+    if (live) {
+      row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, D, t, tpr, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
-    row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, live, D, t, tpr, v);
+      for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
+      row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, D, t, tpr, v);
+    }
   }
 }
 
-// Block: chunk blockIdx.x % chunks of the rows of sample blockIdx.x / chunks.  AHEAD: the next
-// row is requested early (the widest rows have no registers for it).
-template <int E, int NV, bool AHEAD, typename RT, typename CT>
-__global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a, int chunks) {
-  extern __shared__ float dyn[];    // [rows][3][tpr NV] column sums of the row lanes (rows > 1)
+// Block: chunk blockIdx.x % chunks of the rows of sample blockIdx.x / chunks;
+// n = tpr x R row threads and a producer warp.  Wide rows (NV = 24) are read from
+// the ring twice, for their sums and for their gradients: the registers hold
+// column sums and coefficients instead.
+template <int E, int NV, typename RT, typename CT>
+__global__ void __launch_bounds__(NV == 8 ? 512 : 384) res_norm_grad_kernel(const ResNormGrad a, const Ring ring, int chunks, int tpr, int R) {
+  constexpr bool KEEP = NV == 8;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float sh[2 * 16 * 8];
+  __shared__ Bars bars;
   const ResNorm& f = a.f;
-  const int t = threadIdx.x, tpr = blockDim.x, ry = threadIdx.y, R = blockDim.y, D = f.D;
-  const int grp = blockIdx.x / chunks, ck = blockIdx.x % chunks, g_lo = grp * f.rows_per_group, g_n = min(f.rows_per_group, f.M - g_lo);
+  const int n = tpr * R, D = f.D;
+  const int grp = blockIdx.x / chunks, ck = blockIdx.x % chunks, g_lo = grp * f.rows_per_group;
+  const int g_n = min(f.rows_per_group, f.M - g_lo);
   const int lo = g_lo + (int)((long long)g_n * ck / chunks), hi = g_lo + (int)((long long)g_n * (ck + 1) / chunks);
+  bars_init(bars, ring.stages, n / 32);
   pdl_trigger();
   pdl_wait();
-  int phase = 0;
+  if ((int)threadIdx.x >= n) {
+    const int i = threadIdx.x % 32;
+    produce<4>(i == 0 ? f.x : i == 1 ? f.y : i == 2 ? a.dh : a.ds, i == 1 || i == 2 ? sizeof(CT) : sizeof(RT), ring, f.M, D, lo,
+               hi, R, smem, bars);
+    return;
+  }
+  const int ry = threadIdx.x / tpr, t = threadIdx.x - ry * tpr;
+  int phase = 0, st = 0;
+  uint32_t full_phase = 0;
   float mul[NV], w[NV];
   {
     float unused[NV];
@@ -363,60 +375,68 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
   float sa[NV], sb[NV], sq[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) sa[j] = sb[j] = sq[j] = 0.f;
-  Row<E, NV, RT> xs, xd;
-  Row<E, NV, CT> xy, xh;
-  auto load = [&](int m) {
-    if (m < hi) {
-      const size_t o = (size_t)m * D;
-      xs.load(reinterpret_cast<const RT*>(f.x) + o, D, t, tpr);
-      xy.load(reinterpret_cast<const CT*>(f.y) + o, D, t, tpr);
-      xh.load(reinterpret_cast<const CT*>(a.dh) + o, D, t, tpr);
-      if (a.ds) xd.load(reinterpret_cast<const RT*>(a.ds) + o, D, t, tpr);
-    } else {  // (a row lane past the chunk's end: adds nothing)
-      xs.zero(), xy.zero(), xh.zero(), xd.zero();
-    }
-  };
-  xd.zero();
-  if (AHEAD) load(lo + ry);
   const float inv = 1.f / (float)D;
   for (int m0 = lo; m0 < hi; m0 += R) {
     const int m = m0 + ry;
     const bool live = m < hi;
-    if (!AHEAD) load(m);
-    float s[NV], y[NV], ds[NV], dh[NV];
-    xs.get(s, t, tpr, D), xy.get(y, t, tpr, D), xd.get(ds, t, tpr, D), xh.get(dh, t, tpr, D);
-    if (AHEAD) load(m + R);
+    const int Dl = live ? D : 0;  // (a row lane past the chunk's end adds nothing)
+    mbar_wait(&bars.full[st], full_phase, &g_norm_status, kStatusTimeoutTmaFull, (volatile int*)&bars.abort);
+    const uint8_t* stage = smem + (size_t)st * ring.stage_bytes;
+    const RT* ps = staged<RT>(stage, ring.off[0], f.x, m0, D, ry);
+    const CT* py = staged<CT>(stage, ring.off[1], f.y, m0, D, ry);
+    const CT* ph = staged<CT>(stage, ring.off[2], a.dh, m0, D, ry);
+    const RT* pd = staged<RT>(stage, ring.off[3], a.ds, m0, D, ry);
+    const int Dd = a.ds ? Dl : 0;
     float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float s[NV], y[NV], dh[NV], dv[NV];
+    auto get = [&] {
+      row_get<E, NV>(ps, Dl, t, tpr, s);
+      row_get<E, NV>(ph, Dl, t, tpr, dh);
+      row_get<E, NV>(py, Dl, t, tpr, y);
+      row_get<E, NV>(pd, Dd, t, tpr, dv);
+    };
+    auto done = [&] {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.empty[st]);
+      if (++st == ring.stages) st = 0, full_phase ^= 1;
+    };
+    get();
+    if (KEEP) done();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float dn = dh[j] * mul[j];
+      const float dn = dh[j] * mul[j], wy = w[j] * y[j];
       v[0] += s[j] * s[j];
       v[1] += dn * s[j];
-      if (f.post) {
-        const float wy = w[j] * y[j];
-        v[2] += y[j] * y[j];
-        v[3] += wy * ds[j];
-        v[4] += wy * dn;
-        v[5] += wy * s[j];
-      }
+      v[2] += y[j] * y[j];
+      v[3] += wy * dv[j];
+      v[4] += wy * dn;
+      v[5] += wy * s[j];
     }
-    row_sum<6>(v, t, tpr, ry, R, sh, phase);
-    const float r = 1.f / sqrtf(v[0] * inv + kEps);
+    row_sum<6>(v, t, tpr, ry, R, sh, phase, n);
+    const float r = rsqrtf(v[0] * inv + kEps);
     const float c = r * r * r * (v[1] * inv);
-    const float rp = f.post ? 1.f / sqrtf(v[2] * inv + kEps) : 1.f;
+    const float rp = f.post ? rsqrtf(v[2] * inv + kEps) : 1.f;
     const float cy = f.post ? rp * rp * inv * (v[3] + r * v[4] - c * v[5]) : 0.f;
+    if (!KEEP) {
+      get();
+      done();
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float dv = ds[j] + r * dh[j] * mul[j] - s[j] * c;
-      const float q = y[j] * rp;
+      dv[j] = dv[j] + r * dh[j] * mul[j] - s[j] * c;
       sa[j] += dh[j] * s[j] * r;
       sb[j] += dh[j];
-      sq[j] += dv * q;
-      ds[j] = f.alpha * dv;
-      dh[j] = f.post ? rp * (dv * w[j] - y[j] * cy) : dv * w[j];
+      sq[j] += dv[j] * (y[j] * rp);
     }
-    row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, live, D, t, tpr, ds);
-    row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, live, D, t, tpr, dh);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      y[j] = rp * (dv[j] * w[j] - y[j] * cy);  // (rp = 1, cy = 0 without the norm)
+      dv[j] *= f.alpha;
+    }
+    if (live) {
+      row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, dv);
+      row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, y);
+    }
   }
   if (!a.part) return;
   float* part = a.part + (size_t)blockIdx.x * 3 * D;
@@ -428,15 +448,18 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
     }
     return;
   }
+  // the row lanes' sums joined in the ring, which is idle: every row thread is
+  // past its last stage, and so every copy has landed
+  float* dyn = reinterpret_cast<float*>(smem);
   const int W = tpr * NV;
+  row_bar(n);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = elem<E>(t, tpr, j);
-    float* d = dyn + (size_t)ry * 3 * W + i;
+    float* d = dyn + (size_t)ry * 3 * W + elem<E>(t, tpr, j);
     d[0] = sa[j], d[W] = sb[j], d[2 * W] = sq[j];
   }
-  __syncthreads();
-  for (int i = ry * tpr + t; i < 3 * D; i += R * tpr) {
+  row_bar(n);
+  for (int i = threadIdx.x; i < 3 * D; i += n) {
     const int k = i / D, c = i % D;
     float x = 0.f;
     for (int r = 0; r < R; ++r) x += dyn[(size_t)r * 3 * W + k * W + c];
@@ -444,10 +467,11 @@ __global__ void __launch_bounds__(512) res_norm_grad_kernel(const ResNormGrad a,
   }
 }
 
-// Column sums from the partials: 32 columns x 32 lanes.  Few samples: the
-// lanes share each sample's chunks; many: each lane takes whole samples.
+// Column sums from the partials: 32 columns x 32 lanes.  Fewer samples than
+// lanes: 32 / groups lanes share each sample's chunks; more: each lane takes
+// whole samples.
 __global__ void __launch_bounds__(1024) res_norm_sum_kernel(const ResNormGrad a, int groups, int chunks) {
-  __shared__ float sh[2][32][33];
+  __shared__ float sh[3][32][33];
   const ResNorm& f = a.f;
   const int tx = threadIdx.x, ty = threadIdx.y, D = f.D, d = blockIdx.x * 32 + tx;
   pdl_trigger();
@@ -463,83 +487,75 @@ __global__ void __launch_bounds__(1024) res_norm_sum_kernel(const ResNormGrad a,
     tg += (f.scale ? 1.f + f.scale[mo] : 1.f) * A;
     tp += (f.gate ? f.gate[mo] : 1.f) * Q;
   };
-  if (groups >= 32) {
-    if (in)
-      for (int g = ty; g < groups; g += 32) {
-        float A = 0.f, B = 0.f, Q = 0.f;
-        const float* p = a.part + (size_t)g * chunks * 3 * D + d;
-        for (int c = 0; c < chunks; ++c, p += (size_t)3 * D) A += p[0], B += p[D], Q += p[2 * D];
-        emit(g, A, B, Q);
-      }
-  } else {
-    for (int g = 0; g < groups; ++g) {
-      float v[3] = {0.f, 0.f, 0.f};
-      if (in) {
-        const float* p = a.part + ((size_t)g * chunks + ty) * 3 * D + d;
-        for (int c = ty; c < chunks; c += 32, p += (size_t)32 * 3 * D) v[0] += p[0], v[1] += p[D], v[2] += p[2 * D];
-      }
-      float sum[3];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        __syncthreads();
-        sh[0][ty][tx] = v[k];
-        __syncthreads();
-        float x = sh[0][tx][ty];  // lane tx of column ty
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (tx == 0) sh[1][0][ty] = x;
-        __syncthreads();
-        sum[k] = sh[1][0][tx];
-      }
-      if (ty == 0 && in) emit(g, sum[0], sum[1], sum[2]);
+  const int lpg = groups < 32 ? 32 / groups : 1, sub = ty % lpg, used = groups < 32 ? groups * lpg : 32;
+  float A = 0.f, B = 0.f, Q = 0.f;
+  for (int g = ty / lpg; g < groups && ty < used; g += used / lpg) {
+    A = B = Q = 0.f;
+    if (in) {
+      const float* p = a.part + ((size_t)g * chunks + sub) * 3 * D + d;
+#pragma unroll 8
+      for (int c = sub; c < chunks; c += lpg, p += (size_t)lpg * 3 * D) A += p[0], B += p[D], Q += p[2 * D];
+      if (lpg == 1) emit(g, A, B, Q);
     }
-    if (ty == 0 && in) {
-      if (a.dgain) a.dgain[d] = tg;
-      if (a.dpost_gain) a.dpost_gain[d] = tp;
+  }
+  if (lpg > 1) {
+    sh[0][ty][tx] = A, sh[1][ty][tx] = B, sh[2][ty][tx] = Q;
+    __syncthreads();
+    if (ty < groups && in) {
+      A = B = Q = 0.f;
+      for (int l = ty * lpg; l < (ty + 1) * lpg; ++l) A += sh[0][l][tx], B += sh[1][l][tx], Q += sh[2][l][tx];
+      emit(ty, A, B, Q);
     }
-    return;
+    __syncthreads();
   }
   sh[0][ty][tx] = tg;
   sh[1][ty][tx] = tp;
   __syncthreads();
-  if (ty < 2) {
+  if (ty < 2 && in) {
     float x = 0.f;
 #pragma unroll
     for (int r = 0; r < 32; ++r) x += sh[ty][r][tx];
     float* out = ty == 0 ? a.dgain : a.dpost_gain;
-    if (in && out) out[d] = x;
+    if (out) out[d] = x;
   }
 }
 
-// Chunks of rows per sample: about three blocks an SM in all, each of at least
-// four passes of its row lanes.
+// Chunks of rows per sample: as many blocks as run at once (two an SM, one of
+// more than 256 threads), each of at least four passes of its row lanes.
 int grad_chunks(int M, int D, int rpg) {
-  const int rows = rows_at_once(row_threads(D, elems(D)));
+  const int tpr = row_threads(D, elems(D)), rows = rows_at_once(tpr), blocks = tpr * rows <= 224 ? 296 : 148;
   const int groups = (M + rpg - 1) / rpg;
   const int most = (std::min(rpg, M) + 4 * rows - 1) / (4 * rows);
-  return std::max(1, std::min(most, (444 + groups - 1) / groups));
+  return std::max(1, std::min(most, (blocks + groups - 1) / groups));
 }
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
-  const int tpr = row_threads(a.D, NV), R = rows_at_once(tpr);
+  const int tpr = row_threads(a.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
+  const Ring ring = ring_of(a.D, R, {(int)sizeof(RT), (int)sizeof(CT)});
+  const int smem = ring.stages * ring.stage_bytes;
+  auto* kernel = NV == 8 && threads <= 256 ? res_norm_kernel<E, NV, NV == 8, RT, CT> : res_norm_kernel<E, NV, false, RT, CT>;
   int dev = 0, sms = 148, per = 1;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, res_norm_kernel<E, NV, RT, CT>, tpr * R, 0)) != cudaSuccess)
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingWide)) != cudaSuccess ||
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem)) != cudaSuccess)
     return e;
   const int grid = std::max(1, std::min((a.M + R - 1) / R, sms * std::max(1, per)));
-  return launch_k(res_norm_kernel<E, NV, RT, CT>, dim3(grid), dim3(tpr, R), 0, s, a);
+  return launch_k(kernel, dim3(grid), dim3(threads), smem, s, a, ring, tpr, R);
 }
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_bwd(const ResNormGrad& a, int chunks, int groups, cudaStream_t s) {
-  const int tpr = row_threads(a.f.D, NV), R = rows_at_once(tpr);
-  const size_t smem = R > 1 && a.part ? (size_t)R * 3 * tpr * NV * 4 : 0;
-  return launch_k(res_norm_grad_kernel<E, NV, NV == 8, RT, CT>, dim3((unsigned)chunks * groups), dim3(tpr, R), smem, s, a,
-                  chunks);
+  const int tpr = row_threads(a.f.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
+  const Ring ring = ring_of(a.f.D, R, {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
+  const int smem = std::max(ring.stages * ring.stage_bytes, R > 1 ? R * 3 * tpr * NV * 4 : 0);
+  auto* kernel = res_norm_grad_kernel<E, NV, RT, CT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingWide);
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3((unsigned)chunks * groups), dim3(threads), smem, s, a, ring, chunks, tpr, R);
 }
 // f(E, NV, RT, CT) for a call's alignment, width and types.
 template <typename F>
@@ -551,9 +567,9 @@ cudaError_t by_form(bool vec, int D, bool res_f32, bool f32, F f) {
   using std::integral_constant;
   if (elems(D) == 8)
     return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 8>{})
-               : types(integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 16>{})
-             : types(integral_constant<int, 2>{}, integral_constant<int, 16>{});
+               : types(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 24>{})
+             : types(integral_constant<int, 1>{}, integral_constant<int, 24>{});
 }
 
 }  // namespace
@@ -579,6 +595,13 @@ cudaError_t launch_res_norm_grad(const ResNormGrad& a, cudaStream_t s) {
   });
   if (e != cudaSuccess || !a.part) return e;
   return launch_k(res_norm_sum_kernel, dim3((f.D + 31) / 32), dim3(32, 32), 0, s, a, groups, chunks);
+}
+
+cudaError_t res_norm_status(unsigned* bits) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_norm_status, 4);
+  if (e != cudaSuccess || !*bits) return e;
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_norm_status, &zero, 4);
 }
 
 }  // namespace wam
