@@ -408,8 +408,11 @@ class _Args:
     def __call__(self, name: str, x, dtype: int, n: int):
         if x is None or isinstance(x, int):
             return x
-        if not (x.is_cuda and dtype in (FP32, BF16) and x.dtype is _TORCH_TYPES[dtype] and x.numel() == n
-                and x.is_contiguous() and self._here(x)):
+        if self.device == -2:
+            self.device = _torch.cuda.current_device() if _torch.cuda.is_initialized() else -3
+        # (get_device: -1 for a CPU tensor)
+        if not (x.get_device() == self.device and dtype in (FP32, BF16) and x.dtype is _TORCH_TYPES[dtype]
+                and x.numel() == n and x.is_contiguous()):
             self._refuse(name, x, dtype, f"{n} elements")
         return x.data_ptr()
 
@@ -417,7 +420,9 @@ class _Args:
         """fp32 rows of `width` elements, `stride` apart."""
         if x is None or isinstance(x, int):
             return x
-        ok = x.is_cuda and x.dtype is _TORCH_TYPES[FP32] and x.numel() == rows * width and self._here(x)
+        if self.device == -2:
+            self.device = _torch.cuda.current_device() if _torch.cuda.is_initialized() else -3
+        ok = x.get_device() == self.device and x.dtype is _TORCH_TYPES[FP32] and x.numel() == rows * width
         if ok and rows > 1:
             ok = x.dim() == 2 and x.size(0) == rows and x.stride(0) == stride and (x.stride(1) == 1 or width == 1)
         elif ok:
@@ -425,11 +430,6 @@ class _Args:
         if not ok:
             self._refuse(name, x, FP32, f"{rows} rows of {width}, {stride} apart")
         return x.data_ptr()
-
-    def _here(self, x) -> bool:
-        if self.device == -2:
-            self.device = _torch.cuda.current_device()
-        return x.get_device() == self.device
 
     def _refuse(self, name, x, dtype, want):
         kind = _TORCH_TYPES[dtype] if dtype in (FP32, BF16) else dtype
@@ -443,7 +443,7 @@ class _Args:
             return None, 0
         if isinstance(x, int):
             return x, need
-        if not (x.is_cuda and x.is_contiguous() and self._here(x)):
+        if not (x.is_cuda and x.is_contiguous() and x.get_device() == _torch.cuda.current_device()):
             raise WamError(1, self.where, "workspace: need a contiguous CUDA tensor on the current device")
         return x.data_ptr(), x.numel() * x.element_size()
 

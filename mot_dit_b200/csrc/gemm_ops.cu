@@ -677,13 +677,13 @@ struct Device {
   int sms = 148;
   int clusters[9];  // clusters of n CTAs (one per SM) that run at once
 };
-Device g_dev[64];
+Device g_dev[kMaxDevices];
 
 cudaError_t device_info(Device** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   Device& d = g_dev[dev];
   if (!d.ready.load(std::memory_order_acquire)) {  // (idempotent: two threads may both do it)
     int sms = 0;

@@ -4,9 +4,11 @@
 // T x T output tiles (T = 128 or 64), 256 threads, (T / 16)^2 sums a thread in
 // registers, added two at a time (fma.rn.f32x2).  Operands pass through a
 // double-buffered shared tile of 16 reduction indices stored [k][m], whichever
-// of their two dimensions is contiguous in memory.  Few tiles with a long
+// of their two dimensions is contiguous in memory.  Tiles with a long
 // reduction are shared by the CTAs of a cluster, one k-range each; the partial
-// tiles are summed in rank (= k) order through distributed shared memory.
+// tiles are summed in rank (= k) order through distributed shared memory.  In
+// a list of products each is split or not by its own length (the CTAs of a
+// cluster then take a tile each).
 // Bound by the fp32 pipes (2 T^2 / (2 T) flop per shared-memory word).
 #include <algorithm>
 
@@ -23,14 +25,15 @@ struct ProductF {
   OpMat a[2], b[2];
   int M, N, K;   // K: one pair's reduction
   int pairs;
-  int tiles_m, tiles_n, tile0;
+  int tiles_m, tiles, cta0;  // cta0: first CTA, a whole number of clusters
+  int split;                 // CTAs that share a tile (1, or the cluster)
   int a_mn, b_mn, gated, avec, bvec;
   OpEpi e;
 };
 struct ArgsF {
   ProductF p[kOpProducts];
   OpColSum sums[2];
-  int np, n_sums, split;
+  int np, n_sums;
 };
 
 __device__ __forceinline__ void fma2(float2& c, float2 a, float2 b) {
@@ -54,20 +57,21 @@ __device__ __forceinline__ float4 fetch4(const OpMat& m, int r, int c, bool vec)
 }
 
 template <int T>
-__global__ void __launch_bounds__(256) op_gemm_f32_kernel(const __grid_constant__ ArgsF g) {
+__global__ void __launch_bounds__(256, T == 128 ? 2 : 4) op_gemm_f32_kernel(const __grid_constant__ ArgsF g) {
   constexpr int R = T / 16;        // sums per thread and dimension
   constexpr int L = T + 4;         // shared row of one k
   constexpr int F = T * KT / 1024; // float4 per thread, operand and step
   extern __shared__ __align__(16) float sh[];
   float* sA = sh;                  // [2][KT][L]
   float* sB = sh + 2 * KT * L;
-  const int tid = threadIdx.x, S = g.split;
-  const uint32_t rank = S > 1 ? cluster_rank() : 0u;
-  const int t = blockIdx.x / S;
+  const int tid = threadIdx.x;
   int pi = 0;
-  while (pi + 1 < g.np && t >= g.p[pi + 1].tile0) ++pi;
+  while (pi + 1 < g.np && (int)blockIdx.x >= g.p[pi + 1].cta0) ++pi;
   const ProductF& P = g.p[pi];
-  const int l = t - P.tile0, tm = l % P.tiles_m, tn = l / P.tiles_m;
+  const int S = P.split;
+  const uint32_t rank = S > 1 ? cluster_rank() : 0u;
+  const int l = ((int)blockIdx.x - P.cta0) / S, tm = l % P.tiles_m, tn = l / P.tiles_m;
+  const bool idle = l >= P.tiles;  // (fills up a cluster of unsplit tiles)
   const int m0 = tm * T, width = P.gated ? T / 2 : T, n0 = tn * width;
   pdl_trigger();
   pdl_wait();
@@ -80,6 +84,7 @@ __global__ void __launch_bounds__(256) op_gemm_f32_kernel(const __grid_constant_
       cs.out[c] = a;
     }
   }
+  if (idle) return;
 
   const int steps = (P.K + KT - 1) / KT, all = steps * P.pairs;
   const int s_lo = (int)((long long)all * rank / S), s_hi = (int)((long long)all * (rank + 1) / S);
@@ -183,28 +188,45 @@ constexpr int smem_f32() {
 }
 
 template <int T>
-cudaError_t launch_t(ArgsF& g, const OpProduct* p, int n, int split, cudaStream_t s) {
-  int tiles = 0;
+cudaError_t launch_t(ArgsF& g, const OpProduct* p, int n, int sms, cudaStream_t s) {
+  long long tiles[kOpProducts], all = 0;
+  int steps[kOpProducts] = {}, least = 1 << 30;
   for (int i = 0; i < n; ++i) {
     ProductF& k = g.p[i];
     k.tiles_m = (p[i].M + T - 1) / T;
-    k.tiles_n = (p[i].gated ? 2 * p[i].N + T - 1 : p[i].N + T - 1) / T;
-    k.tile0 = tiles;
-    tiles += k.tiles_m * k.tiles_n;
+    k.tiles = k.tiles_m * (int)((p[i].gated ? 2ll * p[i].N + T - 1 : p[i].N + T - 1) / T);
+    tiles[i] = k.tiles;
+    all += tiles[i];
+    steps[i] = k.pairs * ((p[i].K + KT - 1) / KT);
+    least = std::min(least, steps[i]);
   }
-  g.split = split;
-  cudaError_t e = cudaFuncSetAttribute(op_gemm_f32_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_f32<T>());
+  // Cluster: until every SM has four blocks, or the longest reduction is as
+  // short as the others; a share keeps eight steps.
+  int S = 1;
+  if (T == 64) {
+    const int longest = *std::max_element(steps, steps + n);
+    while (S < 8 && longest >= 16 * S && (all * S < 4 * sms || longest > 2 * S * least)) S *= 2;
+  }
+  int cta = 0;
+  for (int i = 0; i < n; ++i) {
+    ProductF& k = g.p[i];
+    k.split = S > 1 && steps[i] >= 8 * S && (all < 2 * sms || steps[i] >= 2 * least) ? S : 1;
+    k.cta0 = cta;
+    cta += (k.tiles * k.split + S - 1) / S * S;
+  }
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(op_gemm_f32_kernel<T>, smem_f32<T>(), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * split);
+  cfg.gridDim = dim3(cta);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem_f32<T>();
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   int na = 0;
-  if (split > 1) {
+  if (S > 1) {
     at[na].id = cudaLaunchAttributeClusterDimension;
-    at[na].val.clusterDim.x = split;
+    at[na].val.clusterDim.x = S;
     at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
     ++na;
   }
@@ -222,18 +244,14 @@ cudaError_t launch_t(ArgsF& g, const OpProduct* p, int n, int split, cudaStream_
 
 cudaError_t launch_op_gemm_f32(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s) {
   if (n < 1 || n > kOpProducts || n_sums < 0 || n_sums > 2) return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return e;
+  const int sms = current_sms();
+  if (!sms) return cudaErrorNoDevice;
   ArgsF g;
   g.np = n;
   g.n_sums = n_sums;
   for (int i = 0; i < n_sums; ++i) g.sums[i] = sums[i];
   auto vec = [](const OpMat& m) { return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.ld % 4 == 0; };
   long long t128 = 0, t64 = 0;
-  int steps = 1 << 30;
   for (int i = 0; i < n; ++i) {
     const OpProduct& q = p[i];
     ProductF& k = g.p[i];
@@ -255,14 +273,11 @@ cudaError_t launch_op_gemm_f32(const OpProduct* p, int n, const OpColSum* sums, 
     const long long cols = q.gated ? 2ll * q.N : q.N;
     t128 += ((q.M + 127ll) / 128) * ((cols + 127) / 128);
     t64 += ((q.M + 63ll) / 64) * ((cols + 63) / 64);
-    steps = std::min(steps, k.pairs * ((q.K + KT - 1) / KT));
   }
-  // A 128-wide tile does a quarter of the tiles' shared-memory traffic of
-  // four 64-wide ones, but needs two for every SM to keep the pipes busy.
-  if (t128 >= 2 * sms) return launch_t<128>(g, p, n, 1, s);
-  int split = 1;
-  while (split < 8 && t64 * split < 2 * sms && steps >= 8 * split) split *= 2;
-  return launch_t<64>(g, p, n, split, s);
+  // A 128-wide tile does a quarter of the shared-memory traffic of four
+  // 64-wide ones but needs two for every SM, in whole rounds.
+  const double w128 = (double)((t128 + 2 * sms - 1) / (2 * sms)) * 8, w64 = (double)((t64 + 4 * sms - 1) / (4 * sms)) * 4 * 1.3;
+  return t128 >= sms && w128 <= w64 ? launch_t<128>(g, p, n, sms, s) : launch_t<64>(g, p, n, sms, s);
 }
 
 }  // namespace wam

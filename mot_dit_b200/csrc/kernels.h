@@ -3,6 +3,7 @@
 // enqueues kernels on the given stream and returns the launch error code.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -28,6 +29,21 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// SMs of the current device (0: no device); looked up once per device.
+int current_sms(int* device = nullptr);
+// Once per device: kernel's shared-memory limit (done[] is the caller's, one per kernel).
+constexpr int kMaxDevices = 64;
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;  // (idempotent: two threads may both do it)
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
 }
 
 // Widest row the RMSNorm / modulation kernels and the GEMM norm prologue take.
@@ -492,6 +508,9 @@ struct ResNormGrad {
 };
 size_t res_norm_part_floats(int M, int D, int rows_per_group);
 cudaError_t launch_res_norm_grad(const ResNormGrad& a, cudaStream_t s);
+// Forward products of few rows: whether the kernels take p, and one launch.
+bool op_skinny_takes(const OpProduct& p, bool f32);
+cudaError_t launch_op_skinny(const OpProduct& p, bool f32, cudaStream_t s);
 // Bits of the bounded waits that gave up on the current device, and clears them (synchronous).
 cudaError_t op_gemm_status(unsigned* bits);
 cudaError_t res_norm_status(unsigned* bits);  // (after a synchronisation)

@@ -396,6 +396,19 @@ bool pdl_enabled() {
   return on;
 }
 
+int current_sms(int* device) {
+  static std::atomic<int> sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 0;
+  if (device) *device = dev;
+  if (!sms[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    sms[dev] = n;
+  }
+  return sms[dev];
+}
+
 // ------------------------------------------------------- tensor maps -------
 namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;

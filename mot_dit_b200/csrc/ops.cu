@@ -58,6 +58,7 @@ void set_vec(OpEpi& e) {
           aligned(e.z, 16) && aligned(e.z2, 16);
 }
 cudaError_t products(int dtype, const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s) {
+  if (n == 1 && n_sums == 0 && op_skinny_takes(p[0], dtype == WAM_FP32)) return launch_op_skinny(p[0], dtype == WAM_FP32, s);
   return dtype == WAM_FP32 ? launch_op_gemm_f32(p, n, sums, n_sums, s) : launch_op_gemm(p, n, sums, n_sums, s);
 }
 

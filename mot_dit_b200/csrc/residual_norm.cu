@@ -537,13 +537,13 @@ cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const Ring ring = ring_of(a.D, R, {(int)sizeof(RT), (int)sizeof(CT)});
   const int smem = ring.stages * ring.stage_bytes;
   auto* kernel = NV == 8 && threads <= 256 ? res_norm_kernel<E, NV, NV == 8, RT, CT> : res_norm_kernel<E, NV, false, RT, CT>;
-  int dev = 0, sms = 148, per = 1;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingWide)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem)) != cudaSuccess)
-    return e;
+  static std::atomic<bool> done[2][kMaxDevices];
+  const cudaError_t e = allow_smem(kernel, kRingWide, done[NV == 8 && threads <= 256]);
+  if (e != cudaSuccess) return e;
+  const int sms = current_sms();
+  if (!sms) return cudaErrorNoDevice;
+  // as many blocks as run at once: by registers (see the launch bounds) and by shared memory
+  const int per = std::min(threads > 256 ? 1 : NV == 8 ? (E == 8 ? 3 : 2) : 1, 227 * 1024 / (smem + 3072));
   const int grid = std::max(1, std::min((a.M + R - 1) / R, sms * std::max(1, per)));
   return launch_k(kernel, dim3(grid), dim3(threads), smem, s, a, ring, tpr, R);
 }
@@ -553,7 +553,8 @@ cudaError_t run_bwd(const ResNormGrad& a, int chunks, int groups, cudaStream_t s
   const Ring ring = ring_of(a.f.D, R, {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
   const int smem = std::max(ring.stages * ring.stage_bytes, R > 1 ? R * 3 * tpr * NV * 4 : 0);
   auto* kernel = res_norm_grad_kernel<E, NV, RT, CT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingWide);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(kernel, kRingWide, done);
   if (e != cudaSuccess) return e;
   return launch_k(kernel, dim3((unsigned)chunks * groups), dim3(threads), smem, s, a, ring, chunks, tpr, R);
 }
