@@ -47,7 +47,10 @@ constexpr int BK = 64;
 constexpr int kABytes = BM * BK * 2;
 constexpr int kEpiWarps = 8;       // two per 32-row quarter of the tile, on alternate 32-column chunks
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kLoaders = 128;      // MANUAL: loader threads
+constexpr int kLoaders = 128;      // loader threads of kManual
+// How operands come in: by TMA; by loader warps (bf16 at any alignment); by
+// the epilogue warps, fp32 in three bf16 parts.
+enum : int { kTma = 0, kManual = 1, kF32 = 2 };
 constexpr int kStg = 32 * 32 * 4;  // staging of one epilogue warp: 32 rows x 32 fp32
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 232448;
@@ -73,7 +76,8 @@ struct GemmArgs {
   int stages, stage_bytes;
   int subs, sub_bytes;  // k-blocks of a full stage, and the bytes of one
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
-  int nbuf, nseg;  // accumulator buffers, and segments of each
+  int nbuf, buf_cols;  // accumulator buffers
+  int nseg;            // segments of a tile's reduction
   int tm_cols;  // tensor-memory columns to allocate
 };
 
@@ -99,6 +103,23 @@ __device__ __forceinline__ void tc_commit_both(uint32_t addr) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(addr),
       "h"((unsigned short)3)
       : "memory");
+}
+
+// 32 lanes x 32 consecutive columns to tensor memory.
+__device__ __forceinline__ void tmem_st32f(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // One thread of a converged warp.  (The compiler recognises the election and
@@ -168,21 +189,36 @@ __device__ __forceinline__ void out_bf16(const float (&v)[32], void* out, const 
   __syncwarp();
 }
 // The residual's elements that this lane will add (requested before the
-// accumulator is read).
-template <typename T>
+// accumulator is read): four of each of eight rows, unconverted.
 struct ResidualVec {
-  Raw<T, 4> r[8];
+  uint4 r[8];
+  template <typename T>
   __device__ __forceinline__ void load(const void* res, const Window& w, int lane) {
     const int n = w.n0 + 4 * (lane & 7);
     const T* p = reinterpret_cast<const T*>(res) + (size_t)(w.m0 + (lane >> 3)) * w.ld + n;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (w.m0 + 4 * i + (lane >> 3) < w.M && n < w.N) r[i].load(p + (size_t)(4 * i) * w.ld);
+    for (int i = 0; i < 8; ++i) {
+      if (w.m0 + 4 * i + (lane >> 3) >= w.M || n >= w.N) continue;
+      if constexpr (sizeof(T) == 4) {
+        r[i] = *reinterpret_cast<const uint4*>(p + (size_t)(4 * i) * w.ld);
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + (size_t)(4 * i) * w.ld);
+        r[i].x = x.x, r[i].y = x.y;
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(int i, float (&z)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+      z[0] = __uint_as_float(r[i].x), z[1] = __uint_as_float(r[i].y), z[2] = __uint_as_float(r[i].z), z[3] = __uint_as_float(r[i].w);
+    } else {
+      z[0] = bf16_lo(r[i].x), z[1] = bf16_hi(r[i].x), z[2] = bf16_lo(r[i].y), z[3] = bf16_hi(r[i].y);
+    }
   }
 };
 // v (+ residual) as T.
 template <typename T>
-__device__ __forceinline__ void out_stream(const float (&v)[32], void* out, const void* res, const ResidualVec<T>& rv,
+__device__ __forceinline__ void out_stream(const float (&v)[32], void* out, const void* res, const ResidualVec& rv,
                                            const Window& w, uint8_t* stg, int lane) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) *stg32(stg, lane, q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
@@ -199,7 +235,7 @@ __device__ __forceinline__ void out_stream(const float (&v)[32], void* out, cons
       if (w.m0 + r < w.M && n < w.N) {
         if (res) {
           float z[4];
-          rv.r[i].get(z);
+          rv.get<T>(i, z);
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] += z[j];
         }
@@ -230,6 +266,16 @@ __device__ __forceinline__ void out_stream(const float (&v)[32], void* out, cons
   }
   __syncwarp();
 }
+// In the operands' type, no residual.
+template <bool F32>
+__device__ __forceinline__ void out_same(const float (&v)[32], void* out, const Window& w, uint8_t* stg, int lane) {
+  if constexpr (F32) {
+    const ResidualVec none{};
+    out_stream<float>(v, out, nullptr, none, w, stg, lane);
+  } else {
+    out_bf16(v, out, w, stg, lane);
+  }
+}
 // Adds bias[n0 ..] to 32 columns (all lanes read the same words).
 __device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int n0, int N, int vec) {
   if (!bias) return;
@@ -248,11 +294,119 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const float* bias, int 
   }
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Whether any thread of the epilogue warps says so (and a barrier of them).
+__device__ __forceinline__ bool epi_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(32 * kEpiWarps)
+      : "memory");
+  return r != 0;
+}
 
-template <int CG, bool MANUAL>
-__global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op_gemm_kernel(const __grid_constant__ GemmArgs g) {
-  static_assert(CG == 1 || !MANUAL, "the loader warps serve single CTAs");
+// ---- fp32 operands as bf16 parts: x = hi + mid + lo, each the nearest bf16 of
+// what the ones before leave, exact for normal numbers (3 x 8 bits).  Six of
+// the nine products are taken; the other three are below 2^-26 of the exact
+// one.  What rounds to an infinite hi has no other parts (an infinity times
+// a zero part still makes NaN of an infinite operand's row or column).
+struct Feed {
+  int it = 0, st = 0;
+  uint32_t phase = 0;
+};
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16(x, y);
+  float a = x - bf16_lo(hi), b = y - bf16_hi(hi);
+  a = fabsf(a) <= 3.4e38f ? a : 0.f;
+  b = fabsf(b) <= 3.4e38f ? b : 0.f;
+  mid = pack_bf16(a, b);
+  lo = pack_bf16(a - bf16_lo(mid), b - bf16_hi(mid));
+}
+// Eight elements [col, col + 8) of a row, zero outside the matrix.
+__device__ __forceinline__ void fetch8_f32(const OpMat& m, int row, int col, float4& x, float4& y) {
+  x = y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row >= m.outer || col >= m.inner) return;
+  const float* p = reinterpret_cast<const float*>(m.p) + (size_t)row * m.ld + col;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && col + 8 <= m.inner) {
+    x = reinterpret_cast<const float4*>(p)[0];
+    y = reinterpret_cast<const float4*>(p)[1];
+    return;
+  }
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = col + j < m.inner ? p[j] : 0.f;
+  x = make_float4(v[0], v[1], v[2], v[3]);
+  y = make_float4(v[4], v[5], v[6], v[7]);
+}
+// k-blocks [lo, hi) of a 128 x BN tile: 256 threads, 16-byte chunks of the
+// swizzled tiles; the next block's elements are requested as soon as the
+// present ones are on their way to shared memory.
+template <int BN>
+__device__ __forceinline__ void feed_f32(const ProductK& P, int m0, int n0, int lo, int hi, int te, uint8_t* smem, int sbytes,
+                                         int stages, uint64_t* full, uint64_t* empty, Feed& f, unsigned* status,
+                                         volatile int* abort) {
+  constexpr int NA = 4, NB = BN / 32, PB = BN * BK * 2;
+  const bool amn = P.a_mn, bmn = P.b_mn, gated = P.gated;
+  const int kb0 = P.kb0;
+  float4 v[NA + NB][2];
+  auto load = [&](int kb) {
+    const int q = kb >= kb0 ? 1 : 0, kk = (kb - (q ? kb0 : 0)) * BK;
+    const OpMat A = P.a[q], B0 = P.b[gated ? 0 : q], B1 = P.b[gated ? 1 : q];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int c = te + i * 256, r = c >> 3, k = (c & 7) * 8;
+      if (amn)
+        fetch8_f32(A, kk + (r & 63), m0 + (r >> 6) * 64 + k, v[i][0], v[i][1]);
+      else
+        fetch8_f32(A, m0 + r, kk + k, v[i][0], v[i][1]);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int c = te + i * 256, r = c >> 3, k = (c & 7) * 8;
+      if (bmn)
+        fetch8_f32(B0, kk + (r & 63), n0 + (r >> 6) * 64 + k, v[NA + i][0], v[NA + i][1]);
+      else if (gated)
+        fetch8_f32(r < BN / 2 ? B0 : B1, n0 + r % (BN / 2), kk + k, v[NA + i][0], v[NA + i][1]);
+      else
+        fetch8_f32(B0, n0 + r, kk + k, v[NA + i][0], v[NA + i][1]);
+    }
+  };
+  load(lo);
+  for (int kb = lo; kb < hi; ++kb, ++f.it) {
+    if (f.it >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[f.st], f.phase ^ 1, status, kStatusTimeoutTmaEmpty, abort)))
+      return;
+    uint8_t* st = smem + (size_t)f.st * sbytes;
+#pragma unroll
+    for (int i = 0; i < NA + NB; ++i) {
+      const int c = te + (i < NA ? i : i - NA) * 256, r = c >> 3;
+      uint8_t* d = st + (i < NA ? 0 : 3 * kABytes) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      const int plane = i < NA ? kABytes : PB;
+      const float4 x = v[i][0], y = v[i][1];
+      uint4 h, m, l;
+      split2(x.x, x.y, h.x, m.x, l.x);
+      split2(x.z, x.w, h.y, m.y, l.y);
+      split2(y.x, y.y, h.z, m.z, l.z);
+      split2(y.z, y.w, h.w, m.w, l.w);
+      *reinterpret_cast<uint4*>(d) = h;
+      *reinterpret_cast<uint4*>(d + plane) = m;
+      *reinterpret_cast<uint4*>(d + 2 * plane) = l;
+    }
+    if (kb + 1 < hi) load(kb + 1);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((te & 31) == 0) mbar_arrive(&full[f.st]);
+    if (++f.st == stages) f.st = 0, f.phase ^= 1;
+  }
+}
+
+
+template <int CG, int MODE>
+__global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThreads, 1) op_gemm_kernel(const __grid_constant__ GemmArgs g) {
+  constexpr bool F32 = MODE == kF32, TMA = MODE == kTma;
+  static_assert(CG == 1 || TMA, "loads by threads serve single CTAs");
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle is a function of the address bits
     if (threadIdx.x == 0) atomicOr(&g_op_status, kStatusTimeoutDrain);
@@ -276,7 +430,7 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(&full[s], MANUAL ? 4 : 1);
+      mbar_init(&full[s], TMA ? 1 : MODE == kManual ? kLoaders / 32 : kEpiWarps);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -286,7 +440,7 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0 && !MANUAL) {
+  if (warp == 0 && lane == 0 && TMA) {
     for (int p = 0; p < g.np; ++p) {
       prefetch_tensormap(&g.p[p].ma[0]);
       prefetch_tensormap(&g.p[p].mb[0]);
@@ -306,10 +460,12 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
   if (CG == 2) cluster_sync();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // Accumulator buffers, nseg segments each: a segment takes up to seg_blocks
-  // k-blocks, and the epilogue adds them (the tensor core's additions truncate,
-  // which a long chain would show in an fp32 output).
-  const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.tm_cols / nbuf;
+  // Accumulator buffers.  A tile's reduction goes through nseg segments of up to
+  // seg_blocks k-blocks (the tensor core's additions truncate, which a long
+  // chain would show in an fp32 output): each fills a buffer of its own, and the
+  // epilogue warps add them up while the next one runs.  fp32 operands:
+  // the segments, and the small products, lie side by side in one.
+  const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.buf_cols;
   auto seg_blocks = [&](int n_kb) {  // (whole stages)
     return ((n_kb + nseg - 1) / nseg + g.subs - 1) / g.subs * g.subs;
   };
@@ -320,7 +476,7 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
   auto k_hi = [&](const ProductK& P) { return S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb; };
 
   if (warp == 0) {
-    if (!MANUAL && elect_one()) {
+    if (TMA && elect_one()) {
       const bool peer = CG == 2 && rank == 1;
       int it = 0, st = 0;  // stages filled; the next one and its phase
       uint32_t phase = 0;
@@ -397,7 +553,7 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
       int st = 0, buf = 0, lt = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
-      for (int t = unit; t < g.tiles && ok; t += units, ++lt) {
+      for (int t = unit; t < g.tiles && ok; t += units) {  // lt: buffers filled
         const ProductK& P = g.p[tile_at(g, t).p];
         if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) break;
         tc_fence_after();
@@ -410,10 +566,38 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
         uint32_t d = tmem + buf * buf_cols;
         int in = 0;  // k-blocks in the present segment
         for (int kb = lo; kb < hi;) {
+          if (!F32 && kb > lo && in == 0) {  // the next segment's buffer is drained
+            if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d = tmem + buf * buf_cols;
+          }
           if (!mbar_wait(&full[st], phase, status, kStatusTimeoutTmaFull, abort_flag)) {
             ok = false;
             break;
           }
+          if constexpr (F32) {
+            // parts: A hi, mid, lo, then B's.  hi hi goes to the segment's
+            // accumulator, the five smaller products to the last one, whose
+            // truncations are 2^-8 of the others'.
+            const uint32_t a0 = smem0 + (uint32_t)(st * sbytes), pb = bn * BK * 2;
+            const uint32_t dx = tmem + nseg * bn;
+            auto mma = [&](int i, int j, uint32_t to, uint32_t acc0) {
+              const uint64_t da = da0 | ((a0 + i * kABytes) >> 4 & 0x3FFF);
+              const uint64_t db = db0 | ((a0 + 3 * kABytes + j * pb) >> 4 & 0x3FFF);
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(to, da + k * sa, db + k * sb, idesc, k > 0 ? 1u : acc0);
+            };
+            mma(0, 0, d, in > 0);
+            mma(0, 2, dx, kb > lo);
+            mma(2, 0, dx, 1);
+            mma(1, 1, dx, 1);
+            mma(0, 1, dx, 1);
+            mma(1, 0, dx, 1);
+            ++in, ++kb;
+          } else {
           const int ns = min(subs, (kb < kb0 ? min(hi, kb0) : hi) - kb);  // (a stage never spans two operand pairs)
           uint32_t a0 = smem0 + (uint32_t)(st * sbytes);
           for (int i = 0; i < ns; ++i, ++kb, a0 += sub_bytes) {
@@ -429,18 +613,24 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
             }
             ++in;
           }
+          }
           if constexpr (CG == 2)
             tc_commit_both(smem_u32(&empty[st]));
           else
             tc_commit(&empty[st]);
           if (++st == stages) st = 0, phase ^= 1;
-          if (in >= seg) in = 0, d += bn;
+          if (F32 ? kb >= hi : in >= seg || kb >= hi) {  // a buffer is complete
+            if constexpr (CG == 2)
+              tc_commit_both(smem_u32(&accf[buf]));
+            else
+              tc_commit(&accf[buf]);
+            if (++buf == nbuf) buf = 0, bphase ^= 1;
+            ++lt;
+            in = 0;
+          } else if (F32 && in >= seg) {
+            in = 0, d += bn;
+          }
         }
-        if constexpr (CG == 2)
-          tc_commit_both(smem_u32(&accf[buf]));
-        else
-          tc_commit(&accf[buf]);
-        if (++buf == nbuf) buf = 0, bphase ^= 1;
       }
     }
     __syncwarp();
@@ -460,29 +650,86 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
     uint8_t* stg = sStg + (warp - 2) * kStg;
     int buf = 0;
     uint32_t bphase = 0;
+    Feed feed;
     for (int t = unit; t < g.tiles; t += units) {
       const Tile tl = tile_at(g, t);
       const ProductK& P = g.p[tl.p];
+      if constexpr (F32) {  // these warps bring the operands in first
+        if (P.bn == 128)
+          feed_f32<128>(P, tl.m * BM, tl.n * (P.gated ? 64 : 128), k_lo(P), k_hi(P), te, smem, sbytes, stages, full, empty, feed,
+                        status, abort_flag);
+        else
+          feed_f32<64>(P, tl.m * BM, tl.n * (P.gated ? 32 : 64), k_lo(P), k_hi(P), te, smem, sbytes, stages, full, empty, feed,
+                       status, abort_flag);
+      }
       const OpEpi e = P.e;
       const int bn = P.bn, pM = P.M, pN = P.N;
       const bool gated = P.gated;
       const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
       const int n0 = tl.n * (gated ? bn / 2 : bn);
       const int n_kb = k_hi(P) - k_lo(P), sg = seg_blocks(n_kb), segs = (n_kb + sg - 1) / sg;
-      const bool ok = mbar_wait(&accf[buf], bphase, status, kStatusTimeoutAccum, abort_flag);
-      tc_fence_after();
-      if (!ok) *abort_flag = 1;
-      epi_sync();  // one decision for all four warps
-      if (*abort_flag) break;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * buf_cols;
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       const int mw = m0 + quad * 32;
+      auto ready = [&] {  // the present buffer is complete (one decision for all warps)
+        const bool ok = mbar_wait(&accf[buf], bphase, status, kStatusTimeoutAccum, abort_flag);
+        tc_fence_after();
+        const bool stop = epi_any(!ok || *abort_flag);
+        if (stop) *abort_flag = 1;
+        return !stop;
+      };
+      auto drained = [&] {  // this warp's reads of the accumulator are done
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && rank == 1)
+            mbar_arrive_cluster(cluster_addr(&acce[buf], 0));
+          else
+            mbar_arrive(&acce[buf]);
+        }
+      };
+      // segments but the last: summed in tensor memory, behind the buffers (in
+      // registers the sums took those of the rest of the epilogue)
+      const uint32_t t_sum = t_lane + nbuf * buf_cols;
+      bool stop = false;
+      if constexpr (!F32) {
+        for (int k = 0; k + 1 < segs; ++k) {
+          stop = !ready();
+          if (stop) break;
+#pragma unroll 1
+          for (int c = 32 * half; c < bn; c += 64) {
+            float w[32];
+            tmem_ld32(t_lane + buf * buf_cols + c, w);
+            if (k > 0) {
+              float x[32];
+              tmem_ld32(t_sum + c, x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] += x[j];
+            }
+            tmem_st32f(t_sum + c, w);
+          }
+          drained();
+          if (++buf == nbuf) buf = 0, bphase ^= 1;
+        }
+      }
+      if (stop || !ready()) break;
+      const uint32_t t_row = t_lane + buf * buf_cols;
       // 32 accumulator columns, the segments added
       auto acc32 = [&](int c, float (&v)[32]) {
         tmem_ld32(t_row + c, v);
-#pragma unroll 1
-        for (int k = 1; k < segs; ++k) {
+        if constexpr (F32) {
           float w[32];
-          tmem_ld32(t_row + k * bn + c, w);
+          tmem_ld32(t_row + nseg * bn + c, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += w[i];
+#pragma unroll 1
+          for (int k = 1; k < segs; ++k) {
+            tmem_ld32(t_row + k * bn + c, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += w[i];
+          }
+        } else if (segs > 1) {
+          float w[32];
+          tmem_ld32(t_sum + c, w);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] += w[i];
         }
@@ -506,16 +753,6 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
       // 32 output columns at a time: everything but the residual in registers
       // (a row per lane), then through the staging
       const int width = gated ? bn / 2 : bn;
-      auto drained = [&] {  // this warp's reads of the accumulator are done
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2 && rank == 1)
-            mbar_arrive_cluster(cluster_addr(&acce[buf], 0));
-          else
-            mbar_arrive(&acce[buf]);
-        }
-      };
       if (32 * half >= width) drained();  // (a 32-column tile: nothing for the second half)
       for (int c = 32 * half; c < width; c += 64) {
         Window w{mw, pM, n0 + c, pN, e.ld, e.vec};
@@ -523,46 +760,50 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
         float v[32];
         if (gated) {
           float u[32];
-          acc32(c, v);
-          acc32(bn / 2 + c, u);
+          if constexpr (F32) {
+            acc32(c, v);
+            acc32(bn / 2 + c, u);
+          } else {  // (its output is never fp32: one segment)
+            tmem_ld32(t_row + c, v);
+            tmem_ld32(t_row + bn / 2 + c, u);
+          }
           if (c + 64 >= width) drained();
           if (!live) continue;
           add_bias(v, e.bias, w.n0, pN, e.vec);
           add_bias(u, e.bias2, w.n0, pN, e.vec);
           if (e.z) {
-            out_bf16(v, e.z, w, stg, lane);
-            out_bf16(u, e.z2, w, stg, lane);
+            out_same<F32>(v, e.z, w, stg, lane);
+            out_same<F32>(u, e.z2, w, stg, lane);
           }
-          act_apply<true, 32>(e.act, v);
+          act_apply<!F32, 32>(e.act, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= u[j];
-          out_bf16(v, e.out, w, stg, lane);
+          out_same<F32>(v, e.out, w, stg, lane);
         } else {
-          ResidualVec<float> rf;
-          ResidualVec<__nv_bfloat16> rb;
+          ResidualVec rv;
           if (e.res && live && e.vec) {
-            if (e.out_f32)
-              rf.load(e.res, w, lane);
+            if (F32 || e.out_f32)
+              rv.load<float>(e.res, w, lane);
             else
-              rb.load(e.res, w, lane);
+              rv.load<__nv_bfloat16>(e.res, w, lane);
           }
           acc32(c, v);
           if (c + 64 >= width) drained();
           if (!live) continue;
           add_bias(v, e.bias, w.n0, pN, e.vec);
-          if (e.z) out_bf16(v, e.z, w, stg, lane);
-          act_apply<true, 32>(e.act, v);
-          if (e.out_f32)
-            out_stream<float>(v, e.out, e.res, rf, w, stg, lane);
+          if (e.z) out_same<F32>(v, e.z, w, stg, lane);
+          act_apply<!F32, 32>(e.act, v);
+          if (F32 || e.out_f32)
+            out_stream<float>(v, e.out, e.res, rv, w, stg, lane);
           else if (e.res)
-            out_stream<__nv_bfloat16>(v, e.out, e.res, rb, w, stg, lane);
+            out_stream<__nv_bfloat16>(v, e.out, e.res, rv, w, stg, lane);
           else
             out_bf16(v, e.out, w, stg, lane);
         }
       }
       if (++buf == nbuf) buf = 0, bphase ^= 1;
     }
-  } else if (MANUAL) {
+  } else if (MODE == kManual) {
     // ------------------------------------------------------------- loaders
     pdl_wait();
     const int tl_ = threadIdx.x - kThreads;
@@ -637,14 +878,14 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
       const OpEpi e = P.e;
       if (P.gated) {
         if (e.vec)
-          finish_split<false, true, 4>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
+          finish_split<F32, true, 4>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, true, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
+          finish_split<F32, true, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
       } else {
         if (e.vec)
-          finish_split<false, false, 8>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
+          finish_split<F32, false, 8>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
         else
-          finish_split<false, false, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
+          finish_split<F32, false, 1>(e, P.bn, P.N, base, S, te, 32 * kEpiWarps, r_lo, r_hi, m0, n0);
       }
     }
   }
@@ -655,7 +896,11 @@ __global__ void __launch_bounds__(MANUAL ? kThreads + kLoaders : kThreads, 1) op
   if (warp == 1) {
     if (lane == 0) {  // the last commits have arrived before the tensor memory is freed
       int n = 0;
-      for (int t = unit; t < g.tiles; t += units) ++n;
+      for (int t = unit; t < g.tiles; t += units) {
+        const ProductK& P = g.p[tile_at(g, t).p];
+        const int n_kb = k_hi(P) - k_lo(P), sg = seg_blocks(n_kb);
+        n += F32 ? 1 : (n_kb + sg - 1) / sg;
+      }
       for (int l = max(0, n - nbuf); l < n; ++l)
         mbar_wait(&accf[l % nbuf], (l / nbuf) & 1, status, kStatusTimeoutDrain, nullptr);
     }
@@ -688,9 +933,10 @@ cudaError_t device_info(Device** out) {
   if (!d.ready.load(std::memory_order_acquire)) {  // (idempotent: two threads may both do it)
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(op_gemm_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(op_gemm_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(op_gemm_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(op_gemm_kernel<1, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(op_gemm_kernel<2, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(op_gemm_kernel<1, kManual>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(op_gemm_kernel<1, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess)
       return e;
     for (int n = 1; n <= 8; ++n) {
       cudaLaunchConfig_t cfg = {};
@@ -704,8 +950,8 @@ cudaError_t device_info(Device** out) {
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int c = 0;
-      e = n == 2 ? cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<2, false>, &cfg)
-                 : cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<1, false>, &cfg);
+      e = n == 2 ? cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<2, kTma>, &cfg)
+                 : cudaOccupancyMaxActiveClusters(&c, op_gemm_kernel<1, kTma>, &cfg);
       if (e != cudaSuccess) return e;
       d.clusters[n] = std::max(1, std::min(c, sms / n));
     }
@@ -720,9 +966,10 @@ struct Plan {
   int cg, bn, split;
   int seg;  // accumulator segments
 };
-// Longest chain of k-blocks in one accumulator when the output is fp32: 1536
-// products, about 8e-7 of the result in truncated additions (6144: 3e-6).
-constexpr int kChain = 24;
+// Longest chain of k-blocks in one accumulator when the output is fp32: 896
+// products, about 9e-7 of the result in truncated additions (1536: 1.2e-6, 6144: 3e-6).
+constexpr int kChain = 14;
+constexpr int kChainF32 = 12;  // fp32 operands: 768
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Accumulator columns of product p's tiles under plan width bn.
@@ -735,8 +982,8 @@ int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, B
 
 // Estimated ns of a plan, from measured parts: one k-block of a tile (all SMs
 // busy, operands from L2), what follows a tile's last MMA, and the launch.
-double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
-  const double per = pl.cg == 2 ? (pl.bn == 256 ? 370 : 270) : pl.bn == 256 ? 410 : pl.bn == 128 ? 250 : 180;
+double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int mode) {
+  const double per = mode == kF32 ? (pl.bn == 128 ? 950 : 700) : pl.cg == 2 ? (pl.bn == 256 ? 370 : 270) : pl.bn == 256 ? 410 : pl.bn == 128 ? 250 : 180;
   const double tail = 11.0 * pl.bn + 600;
   if (pl.split > 1) {
     const OpProduct& q = p[0];
@@ -745,7 +992,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
     return waves * (ceil_div(k_blocks(q), pl.split) * per + tail + 2500);
   }
   const int units = pl.cg == 2 ? d.clusters[2] : d.sms;
-  const bool bare = 2 * pl.seg * pl.bn > 512;  // one accumulator buffer: every tile's epilogue stands alone
+  const bool bare = mode == kF32;  // one accumulator buffer: every tile's epilogue stands alone
   const double extra = bare ? tail : 150;
   if (n == 1) {
     const int bn = tile_cols(p[0], pl), cols = p[0].gated ? 2 * p[0].N : p[0].N;
@@ -778,28 +1025,31 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d) {
   return worst + tail;
 }
 
-Plan choose(const OpProduct* p, int n, bool manual, const Device& d) {
+Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
   Plan best{1, 128, 1, 1};
   double bc = 1e30;
   int chain = 0;  // longest reduction that ends in fp32
   for (int i = 0; i < n; ++i)
-    if (p[i].e.out_f32) chain = std::max(chain, k_blocks(p[i]));
+    if (mode == kF32 || p[i].e.out_f32) chain = std::max(chain, k_blocks(p[i]));
   auto consider = [&](Plan pl) {
-    pl.seg = std::max(1, ceil_div(ceil_div(chain, pl.split), kChain));
-    if (pl.seg > 512 / pl.bn) {  // no tensor memory for so many: the narrowest tile takes what there is
+    pl.seg = std::max(1, ceil_div(ceil_div(chain, pl.split), mode == kF32 ? kChainF32 : kChain));
+    if (mode != kF32) {
+      if (pl.seg > 1 && pl.bn > 128) return;  // (two buffers and the sums: no tensor memory for wider tiles)
+    } else if (pl.seg > 512 / pl.bn - 1) {  // no tensor memory for so many: the narrowest tile takes what there is
       if (pl.bn > 64) return;
-      pl.seg = 512 / pl.bn;
+      pl.seg = 512 / pl.bn - 1;
     }
-    const double c = plan_cost(p, n, pl, d);
+    const double c = plan_cost(p, n, pl, d, mode);
     if (c < bc) bc = c, best = pl;
   };
   for (int bn : {256, 128, 64}) {
+    if (mode == kF32 && bn == 256) continue;  // (six parts of a 256-wide tile leave no second stage)
     consider(Plan{1, bn, 1, 1});
     if (n == 1)
       for (int s = 2; s <= 8; ++s)
         if (k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s, 1});
   }
-  if (!manual) {
+  if (mode == kTma) {
     consider(Plan{2, 256, 1, 1});
     consider(Plan{2, 128, 1, 1});
   }
@@ -818,18 +1068,18 @@ cudaError_t op_gemm_status(unsigned* bits) {
   return *bits ? cudaMemcpyToSymbol(g_op_status, &zero, 4) : cudaSuccess;
 }
 
-cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s) {
+cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* sums, int n_sums, cudaStream_t s) {
   if (n < 1 || n > kOpProducts || n_sums < 0 || n_sums > 2) return cudaErrorInvalidValue;
   Device* d = nullptr;
   cudaError_t err = device_info(&d);
   if (err != cudaSuccess) return err;
-  bool manual = false;
+  int mode = f32 ? kF32 : kTma;
   for (int i = 0; i < n; ++i) {
     const int na = p[i].pairs == 2 ? 2 : 1, nb = (p[i].pairs == 2 || p[i].gated) ? 2 : 1;
-    for (int k = 0; k < na; ++k) manual |= !tma_ok(p[i].a[k]);
-    for (int k = 0; k < nb; ++k) manual |= !tma_ok(p[i].b[k]);
+    for (int k = 0; k < na; ++k) if (!f32 && !tma_ok(p[i].a[k])) mode = kManual;
+    for (int k = 0; k < nb; ++k) if (!f32 && !tma_ok(p[i].b[k])) mode = kManual;
   }
-  const Plan pl = choose(p, n, manual, *d);
+  const Plan pl = choose(p, n, mode, *d);
   GemmArgs g;
   g.np = n;
   g.n_sums = n_sums;
@@ -857,7 +1107,7 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int 
       const OpMat& mb = q.b[(q.pairs == 2 || q.gated) ? j : 0];
       k.a[j] = ma;
       k.b[j] = mb;
-      if (manual) continue;
+      if (mode != kTma) continue;
       const int boxb = q.b_mn ? 64 : q.gated ? k.bn / 2 : k.bn / pl.cg;
       if (!make_tmap_rows(&k.ma[j], ma.p, ma.inner, ma.outer, ma.ld, q.a_mn ? 64 : BM) ||
           !make_tmap_rows(&k.mb[j], mb.p, mb.inner, mb.outer, mb.ld, boxb))
@@ -866,21 +1116,22 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int 
   }
   g.tiles = tiles;
   g.split = pl.split;
-  g.sub_bytes = kABytes + bmax / pl.cg * BK * 2;
-  g.subs = !manual && 6 * g.sub_bytes <= kSmemMax - kBarBytes - kEpiWarps * kStg ? 2 : 1;
+  g.sub_bytes = (kABytes + bmax / pl.cg * BK * 2) * (f32 ? 3 : 1);
+  g.subs = mode == kTma && 6 * g.sub_bytes <= kSmemMax - kBarBytes - kEpiWarps * kStg ? 2 : 1;
   g.stage_bytes = g.subs * g.sub_bytes;
   g.stages = std::min(kMaxStages, (kSmemMax - kBarBytes - kEpiWarps * kStg) / g.stage_bytes);
   g.nseg = pl.seg;
-  g.nbuf = pl.split == 1 && 2 * pl.seg * bmax <= 512 ? 2 : 1;
+  g.nbuf = f32 ? 1 : 2;
   g.tm_cols = 32;
-  while (g.tm_cols < g.nbuf * pl.seg * bmax) g.tm_cols *= 2;
+  g.buf_cols = bmax;
+  while (g.tm_cols < (f32 ? pl.seg + 1 : pl.seg > 1 ? 3 : 2) * bmax) g.tm_cols *= 2;
   const size_t smem = (size_t)g.stages * g.stage_bytes + kEpiWarps * kStg + kBarBytes;
 
   const int cluster = pl.cg == 2 ? 2 : pl.split;
   const int units = pl.split > 1 ? tiles : std::min(tiles, pl.cg == 2 ? d->clusters[2] : d->sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * cluster);
-  cfg.blockDim = dim3(manual ? kThreads + kLoaders : kThreads);
+  cfg.blockDim = dim3(mode == kManual ? kThreads + kLoaders : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -898,9 +1149,10 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int 
   }
   cfg.attrs = at;
   cfg.numAttrs = na;
-  if (pl.cg == 2) return cudaLaunchKernelEx(&cfg, op_gemm_kernel<2, false>, g);
-  if (manual) return cudaLaunchKernelEx(&cfg, op_gemm_kernel<1, true>, g);
-  return cudaLaunchKernelEx(&cfg, op_gemm_kernel<1, false>, g);
+  if (pl.cg == 2) return cudaLaunchKernelEx(&cfg, op_gemm_kernel<2, kTma>, g);
+  if (mode == kManual) return cudaLaunchKernelEx(&cfg, op_gemm_kernel<1, kManual>, g);
+  if (mode == kF32) return cudaLaunchKernelEx(&cfg, op_gemm_kernel<1, kF32>, g);
+  return cudaLaunchKernelEx(&cfg, op_gemm_kernel<1, kTma>, g);
 }
 
 }  // namespace wam

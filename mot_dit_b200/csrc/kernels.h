@@ -447,10 +447,8 @@ struct OpColSum {
 };
 
 constexpr int kOpProducts = 3;
-// All products of the list in one launch (bf16 operands, fp32 accumulators).
-cudaError_t launch_op_gemm(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s);
-// The same in fp32 on the CUDA cores.
-cudaError_t launch_op_gemm_f32(const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s);
+// All products of the list in one launch (bf16 or fp32 operands).
+cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* sums, int n_sums, cudaStream_t s);
 
 // dz = dy act'(z) (z null: dz = dy) as the compute type, rows ld_dz apart (dz
 // null: sums only), and per row chunk the column sums of dz before rounding,

@@ -59,7 +59,7 @@ void set_vec(OpEpi& e) {
 }
 cudaError_t products(int dtype, const OpProduct* p, int n, const OpColSum* sums, int n_sums, cudaStream_t s) {
   if (n == 1 && n_sums == 0 && op_skinny_takes(p[0], dtype == WAM_FP32)) return launch_op_skinny(p[0], dtype == WAM_FP32, s);
-  return dtype == WAM_FP32 ? launch_op_gemm_f32(p, n, sums, n_sums, s) : launch_op_gemm(p, n, sums, n_sums, s);
+  return launch_op_gemm(p, n, dtype == WAM_FP32, sums, n_sums, s);
 }
 
 // Workspace of a backward pass, in order: the activation's gradients (one or
