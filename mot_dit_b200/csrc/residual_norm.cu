@@ -33,7 +33,7 @@ constexpr float kEps = 1e-6f;
 constexpr int kRowThreads = 224;  // row threads of a block when a row needs fewer (256 with the producer)
 constexpr int kMaxStages = 8;
 constexpr int kRing = 56 * 1024;      // ring of a block (several blocks an SM) ...
-constexpr int kRingWide = 200 * 1024; // ... when two stages fit it, else this
+constexpr int kSmem = 224 * 1024; // ... when two stages fit it, else what a block can have
 
 __device__ unsigned g_norm_status;
 
@@ -47,14 +47,14 @@ int row_threads(int D, int nv) {
   return p;
 }
 int rows_at_once(int tpr) { return tpr >= kRowThreads ? 1 : kRowThreads / tpr; }
-int elems(int D) { return D > 3840 ? 24 : 8; }  // (blocks of at most 512 / 384 threads)
+int elems(int D) { return D > 7680 ? 24 : D > 3840 ? 16 : 8; }  // (blocks of at most 512, 512, 384 threads)
 
 // The ring's shape: `rows` rows of up to four matrices a stage.
 struct Ring {
   int stages, stage_bytes;
   int off[4];  // of each matrix in a stage
 };
-Ring ring_of(int D, int rows, std::initializer_list<int> sizes) {
+Ring ring_of(int D, int rows, int reserved, std::initializer_list<int> sizes) {
   Ring r{};
   int at = 0, i = 0;
   for (int e : sizes) {
@@ -62,7 +62,7 @@ Ring ring_of(int D, int rows, std::initializer_list<int> sizes) {
     at += (rows * D * e + 15) / 16 * 16 + 16;  // (a span that starts inside a granule takes one more)
   }
   r.stage_bytes = (at + 127) / 128 * 128;
-  const int budget = 2 * r.stage_bytes <= kRing ? kRing : kRingWide;
+  const int budget = 2 * r.stage_bytes <= kRing ? kRing : kSmem - reserved;
   r.stages = std::max(1, std::min(kMaxStages, budget / r.stage_bytes));
   return r;
 }
@@ -73,42 +73,94 @@ template <int E>
 __device__ __forceinline__ int elem(int t, int tpr, int j) {
   return (t + (j / E) * tpr) * E + j % E;
 }
-// This thread's elements of a row in shared memory (zero past its end).
-template <int E, int NV, typename T>
-__device__ __forceinline__ void row_get(const T* p, int D, int t, int tpr, float (&v)[NV]) {
+// Elements [8 k, 8 k + 8) of this thread's columns of a row in shared memory
+// (zero past its end).
+template <int E, typename T>
+__device__ __forceinline__ void row_get(const T* p, int D, int t, int tpr, int k, float (&v)[8]) {
 #pragma unroll
-  for (int k = 0; k < NV / E; ++k) {
-    const int i = elem<E>(t, tpr, E * k);
+  for (int j = 0; j < 8; j += E) {
+    const int i = elem<E>(t, tpr, 8 * k + j);
     Raw<T, E> r;
     r.zero();
     if (i < D) r.load(p + i);
-    r.get(v + E * k);
+    r.get(v + j);
   }
 }
-template <int E, int NV, typename T>
-__device__ __forceinline__ void row_store(T* p, int D, int t, int tpr, const float (&v)[NV]) {
+template <int E, typename T>
+__device__ __forceinline__ void row_store(T* p, int D, int t, int tpr, int k, const float (&v)[8]) {
 #pragma unroll
-  for (int k = 0; k < NV / E; ++k) {
-    const int i = elem<E>(t, tpr, E * k);
-    if (i < D) store_to<E>(p + i, v + E * k);
+  for (int j = 0; j < 8; j += E) {
+    const int i = elem<E>(t, tpr, 8 * k + j);
+    if (i < D) store_to<E>(p + i, v + j);
   }
 }
-// A column vector's elements of this thread (fill without one).
-template <int E, int NV>
-__device__ __forceinline__ void vec_load(const float* p, float fill, int D, int t, int tpr, float (&v)[NV]) {
+// Elements [8 k, 8 k + 8) of this thread's columns of a vector (fill without one).
+template <int E>
+__device__ __forceinline__ void vec_get(const float* p, float fill, int D, int t, int tpr, int k, float (&v)[8]) {
   if (!p) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = fill;
+    for (int j = 0; j < 8; ++j) v[j] = fill;
   } else if (E == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    row_get<E, NV>(p, D, t, tpr, v);
+    row_get<E>(p, D, t, tpr, k, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = elem<E>(t, tpr, j);
+    for (int j = 0; j < 8; ++j) {
+      const int i = elem<E>(t, tpr, 8 * k + j);
       v[j] = i < D ? p[i] : 0.f;
     }
   }
 }
+// The coefficients of this thread's columns: gain (1 + scale), shift, gate
+// post_gain.  Eight columns: registers; more: shared memory behind the ring,
+// where each thread keeps its own (no barrier).
+template <int E, int NV>
+struct Coef {
+  float r[NV == 8 ? 3 : 1][8];
+  float* s;
+  int D, t, tpr;
+  __device__ __forceinline__ Coef(uint8_t* smem, int D_, int t_, int tpr_)
+      : s(reinterpret_cast<float*>(smem)), D(D_), t(t_), tpr(tpr_) {}
+  __device__ __forceinline__ void put(int which, int k, const float (&v)[8]) {
+    if constexpr (NV == 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[which][j] = v[j];
+    } else {
+      row_store<E>(s + which * ((D + 7) / 8 * 8), D, t, tpr, k, v);
+    }
+  }
+  __device__ __forceinline__ void get(int which, int k, float (&v)[8]) const {
+    if constexpr (NV == 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = r[which][j];
+    } else {
+      row_get<E>(s + which * ((D + 7) / 8 * 8), D, t, tpr, k, v);
+    }
+  }
+  __device__ __forceinline__ void mul(int k, float (&v)[8]) const { get(0, k, v); }
+  __device__ __forceinline__ void w(int k, float (&v)[8]) const { get(1, k, v); }
+  __device__ __forceinline__ void add(int k, float (&v)[8]) const { get(2, k, v); }
+  // Sample grp's coefficients (shift only where the forward's rows are formed).
+  __device__ __forceinline__ void set(const ResNorm& a, int grp) {
+    const size_t o = (size_t)grp * a.ld_mod;
+#pragma unroll
+    for (int k = 0; k < NV / 8; ++k) {
+      float x[8], y[8];
+      vec_get<E>(a.gain, 1.f, D, t, tpr, k, x);
+      vec_get<E>(a.scale ? a.scale + o : nullptr, 0.f, D, t, tpr, k, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= 1.f + y[j];
+      put(0, k, x);
+      vec_get<E>(a.gate ? a.gate + o : nullptr, 1.f, D, t, tpr, k, x);
+      vec_get<E>(a.post ? a.post_gain : nullptr, 1.f, D, t, tpr, k, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= y[j];
+      put(1, k, x);
+      if (!a.s) continue;
+      vec_get<E>(a.shift ? a.shift + o : nullptr, 0.f, D, t, tpr, k, x);
+      put(2, k, x);
+    }
+  }
+};
 
 // Barrier of the block's n row threads (the producer warp is not among them).
 __device__ __forceinline__ void row_bar(int n) { asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory"); }
@@ -161,25 +213,6 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, i
     }
 #pragma unroll
     for (int k = 0; k < 6; ++k) v[k] = s[k];
-  }
-}
-
-// The coefficients of this thread's columns in sample grp: gain (1 + scale),
-// shift, and gate post_gain.
-template <int E, int NV>
-__device__ __forceinline__ void coef(const ResNorm& a, int grp, int t, int tpr, float (&mul)[NV], float (&add)[NV],
-                                     float (&w)[NV]) {
-  const size_t o = (size_t)grp * a.ld_mod;
-  float x[NV], y[NV];
-  vec_load<E, NV>(a.gain, 1.f, a.D, t, tpr, mul);
-  vec_load<E, NV>(a.scale ? a.scale + o : nullptr, 0.f, a.D, t, tpr, x);
-  vec_load<E, NV>(a.shift ? a.shift + o : nullptr, 0.f, a.D, t, tpr, add);
-  vec_load<E, NV>(a.gate ? a.gate + o : nullptr, 1.f, a.D, t, tpr, w);
-  vec_load<E, NV>(a.post ? a.post_gain : nullptr, 1.f, a.D, t, tpr, y);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    mul[j] *= 1.f + x[j];
-    w[j] *= y[j];
   }
 }
 
@@ -279,7 +312,9 @@ __device__ __forceinline__ const T* staged(const uint8_t* stage, int off, const 
 // Block: n = tpr x R row threads and a producer warp; its rows are
 // [M b / grid, M (b + 1) / grid).  RT / CT: the stream's and the compute type.
 template <int E, int NV, bool SMALL, typename RT, typename CT>
-__global__ void __launch_bounds__(SMALL ? 256 : NV == 8 ? 512 : 384, SMALL ? (E == 8 ? 3 : 2) : 1) res_norm_kernel(const ResNorm a, const Ring ring, int tpr, int R) {
+__global__ void __launch_bounds__(SMALL ? 256 : NV == 24 ? 384 : 512, SMALL ? (E == 8 ? 3 : 2) : 1) res_norm_kernel(const ResNorm a, const Ring ring, int tpr, int R) {
+  constexpr bool KEEP = NV == 8 || E == 8;  // the row in registers, else read from the ring for each pass
+  constexpr int NK = KEEP ? NV / 8 : 1, kUnroll = KEEP ? NV / 8 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float sh[2 * 16 * 8];  // [2][rows][warps][8]: at most 16 warps in all
   __shared__ Bars bars;
@@ -297,55 +332,90 @@ __global__ void __launch_bounds__(SMALL ? 256 : NV == 8 ? 512 : 384, SMALL ? (E 
   int phase = 0, st = 0, next = lo + ry;  // (next: first row that needs other coefficients)
   uint32_t full_phase = 0;
   const float inv = 1.f / (float)D;
-  float mul[NV], add[NV], w[NV];
+  Coef<E, NV> cf(smem + ring.stages * ring.stage_bytes, D, t, tpr);
   for (int m0 = lo; m0 < hi; m0 += R) {
     const int m = m0 + ry;
     const bool live = m < hi;  // (dead row lanes keep the barriers company)
     if (live && m >= next) {
       const int g = m / a.rows_per_group;
-      coef<E, NV>(a, g, t, tpr, mul, add, w);
+      cf.set(a, g);
       next = (g + 1) * a.rows_per_group;
     }
     // (a wait that gives up is reported; the rows go on, so that every barrier is met)
     mbar_wait(&bars.full[st], full_phase, &g_norm_status, kStatusTimeoutTmaFull, (volatile int*)&bars.abort);
     const uint8_t* stage = smem + (size_t)st * ring.stage_bytes;
-    float v[NV], q[NV];
-    row_get<E, NV>(staged<RT>(stage, ring.off[0], a.x, m0, D, ry), live ? D : 0, t, tpr, v);
-    row_get<E, NV>(staged<CT>(stage, ring.off[1], a.y, m0, D, ry), live ? D : 0, t, tpr, q);
-    __syncwarp();
-    if ((t & 31) == 0 && (threadIdx.x & 31) == 0) mbar_arrive(&bars.empty[st]);
-    if (++st == ring.stages) st = 0, full_phase ^= 1;
+    const RT* px = staged<RT>(stage, ring.off[0], a.x, m0, D, ry);
+    const CT* py = staged<CT>(stage, ring.off[1], a.y, m0, D, ry);
+    auto done = [&] {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.empty[st]);
+      if (++st == ring.stages) st = 0, full_phase ^= 1;
+    };
+    const int Dl = live ? D : 0;
+    float vv[NK][8], qq[NK][8];
+    if (KEEP) {
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        row_get<E>(px, Dl, t, tpr, k, vv[k]);
+        row_get<E>(py, Dl, t, tpr, k, qq[k]);
+      }
+      done();
+    }
     float s1[1] = {0.f};
     float rp = 1.f;
     if (a.post) {
+#pragma unroll kUnroll
+      for (int k = 0; k < NV / 8; ++k) {
+        float(&q)[8] = qq[KEEP ? k : 0];
+        if (!KEEP) row_get<E>(py, Dl, t, tpr, k, q);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) s1[0] += q[j] * q[j];
+        for (int j = 0; j < 8; ++j) s1[0] += q[j] * q[j];
+      }
       row_sum<1>(s1, t, tpr, ry, R, sh, phase, n);
       rp = rsqrtf(s1[0] * inv + kEps);
     }
     s1[0] = 0.f;
+    auto stream = [&](int k) {  // v = alpha x + w (y r_y)
+      float w[8], (&v)[8] = vv[KEEP ? k : 0], (&q)[8] = qq[KEEP ? k : 0];
+      cf.w(k, w);
+      if (!KEEP) {
+        row_get<E>(px, Dl, t, tpr, k, v);
+        row_get<E>(py, Dl, t, tpr, k, q);
+      }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      v[j] = a.alpha * v[j] + w[j] * (q[j] * rp);
-      s1[0] += v[j] * v[j];
+      for (int j = 0; j < 8; ++j) v[j] = a.alpha * v[j] + w[j] * (q[j] * rp);
+    };
+#pragma unroll kUnroll
+    for (int k = 0; k < NV / 8; ++k) {
+      stream(k);
+      const float(&v)[8] = vv[KEEP ? k : 0];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s1[0] += v[j] * v[j];
     }
     row_sum<1>(s1, t, tpr, ry, R, sh, phase, n);
     const float r = rsqrtf(s1[0] * inv + kEps);
-    if (live) {
-      row_store<E, NV>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, D, t, tpr, v);
+#pragma unroll kUnroll
+    for (int k = 0; k < NV / 8; ++k) {
+      if (!KEEP) stream(k);
+      if (!live) continue;
+      float mul[8], add[8], (&v)[8] = vv[KEEP ? k : 0];
+      cf.mul(k, mul);
+      cf.add(k, add);
+      row_store<E>(reinterpret_cast<RT*>(a.s) + (size_t)m * D, D, t, tpr, k, v);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = v[j] * r * mul[j] + add[j];
-      row_store<E, NV>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, D, t, tpr, v);
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * r * mul[j] + add[j];
+      row_store<E>(reinterpret_cast<CT*>(a.h) + (size_t)m * D, D, t, tpr, k, v);
     }
+    if (!KEEP) done();
   }
 }
 
 // Block: chunk blockIdx.x % chunks of the rows of sample blockIdx.x / chunks;
-// n = tpr x R row threads and a producer warp.  Wide rows (NV = 24) are read from
-// the ring twice, for their sums and for their gradients: the registers hold
-// column sums and coefficients instead.
+// n = tpr x R row threads and a producer warp.  Wide rows (NV > 8) are read from
+// the ring twice, eight columns at a time, for their sums and for their
+// gradients: the registers hold column sums instead.
 template <int E, int NV, typename RT, typename CT>
-__global__ void __launch_bounds__(NV == 8 ? 512 : 384) res_norm_grad_kernel(const ResNormGrad a, const Ring ring, int chunks, int tpr, int R) {
+__global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(const ResNormGrad a, const Ring ring, int chunks, int tpr, int R) {
   constexpr bool KEEP = NV == 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float sh[2 * 16 * 8];
@@ -367,11 +437,8 @@ __global__ void __launch_bounds__(NV == 8 ? 512 : 384) res_norm_grad_kernel(cons
   const int ry = threadIdx.x / tpr, t = threadIdx.x - ry * tpr;
   int phase = 0, st = 0;
   uint32_t full_phase = 0;
-  float mul[NV], w[NV];
-  {
-    float unused[NV];
-    coef<E, NV>(f, grp, t, tpr, mul, unused, w);
-  }
+  Coef<E, NV> cf(smem + ring.stages * ring.stage_bytes, D, t, tpr);
+  cf.set(f, grp);
   float sa[NV], sb[NV], sq[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) sa[j] = sb[j] = sq[j] = 0.f;
@@ -388,55 +455,58 @@ __global__ void __launch_bounds__(NV == 8 ? 512 : 384) res_norm_grad_kernel(cons
     const RT* pd = staged<RT>(stage, ring.off[3], a.ds, m0, D, ry);
     const int Dd = a.ds ? Dl : 0;
     float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float s[NV], y[NV], dh[NV], dv[NV];
-    auto get = [&] {
-      row_get<E, NV>(ps, Dl, t, tpr, s);
-      row_get<E, NV>(ph, Dl, t, tpr, dh);
-      row_get<E, NV>(py, Dl, t, tpr, y);
-      row_get<E, NV>(pd, Dd, t, tpr, dv);
+    float s[8], y[8], dh[8], dv[8], mul[8], w[8];
+    auto get = [&](int k) {
+      row_get<E>(ps, Dl, t, tpr, k, s);
+      row_get<E>(ph, Dl, t, tpr, k, dh);
+      row_get<E>(py, Dl, t, tpr, k, y);
+      row_get<E>(pd, Dd, t, tpr, k, dv);
+      cf.mul(k, mul);
+      cf.w(k, w);
     };
     auto done = [&] {
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.empty[st]);
       if (++st == ring.stages) st = 0, full_phase ^= 1;
     };
-    get();
-    if (KEEP) done();
+#pragma unroll 1
+    for (int k = 0; k < NV / 8; ++k) {
+      get(k);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const float dn = dh[j] * mul[j], wy = w[j] * y[j];
-      v[0] += s[j] * s[j];
-      v[1] += dn * s[j];
-      v[2] += y[j] * y[j];
-      v[3] += wy * dv[j];
-      v[4] += wy * dn;
-      v[5] += wy * s[j];
+      for (int j = 0; j < 8; ++j) {
+        const float dn = dh[j] * mul[j], wy = w[j] * y[j];
+        v[0] += s[j] * s[j];
+        v[1] += dn * s[j];
+        v[2] += y[j] * y[j];
+        v[3] += wy * dv[j];
+        v[4] += wy * dn;
+        v[5] += wy * s[j];
+      }
     }
+    if (KEEP) done();
     row_sum<6>(v, t, tpr, ry, R, sh, phase, n);
     const float r = rsqrtf(v[0] * inv + kEps);
     const float c = r * r * r * (v[1] * inv);
     const float rp = f.post ? rsqrtf(v[2] * inv + kEps) : 1.f;
     const float cy = f.post ? rp * rp * inv * (v[3] + r * v[4] - c * v[5]) : 0.f;
-    if (!KEEP) {
-      get();
-      done();
-    }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      dv[j] = dv[j] + r * dh[j] * mul[j] - s[j] * c;
-      sa[j] += dh[j] * s[j] * r;
-      sb[j] += dh[j];
-      sq[j] += dv[j] * (y[j] * rp);
-    }
+    for (int k = 0; k < NV / 8; ++k) {
+      if (!KEEP) get(k);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      y[j] = rp * (dv[j] * w[j] - y[j] * cy);  // (rp = 1, cy = 0 without the norm)
-      dv[j] *= f.alpha;
+      for (int j = 0; j < 8; ++j) {
+        dv[j] = dv[j] + r * dh[j] * mul[j] - s[j] * c;
+        sa[8 * k + j] += dh[j] * s[j] * r;
+        sb[8 * k + j] += dh[j];
+        sq[8 * k + j] += dv[j] * (y[j] * rp);
+        y[j] = rp * (dv[j] * w[j] - y[j] * cy);  // (rp = 1, cy = 0 without the norm)
+        dv[j] *= f.alpha;
+      }
+      if (live) {
+        row_store<E>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, k, dv);
+        row_store<E>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, k, y);
+      }
     }
-    if (live) {
-      row_store<E, NV>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, dv);
-      row_store<E, NV>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, y);
-    }
+    if (!KEEP) done();
   }
   if (!a.part) return;
   float* part = a.part + (size_t)blockIdx.x * 3 * D;
@@ -534,11 +604,12 @@ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const int tpr = row_threads(a.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
-  const Ring ring = ring_of(a.D, R, {(int)sizeof(RT), (int)sizeof(CT)});
-  const int smem = ring.stages * ring.stage_bytes;
+  const int coef = NV == 8 ? 0 : 3 * ((a.D + 7) / 8 * 8) * 4;
+  const Ring ring = ring_of(a.D, R, coef, {(int)sizeof(RT), (int)sizeof(CT)});
+  const int smem = ring.stages * ring.stage_bytes + coef;
   auto* kernel = NV == 8 && threads <= 256 ? res_norm_kernel<E, NV, NV == 8, RT, CT> : res_norm_kernel<E, NV, false, RT, CT>;
   static std::atomic<bool> done[2][kMaxDevices];
-  const cudaError_t e = allow_smem(kernel, kRingWide, done[NV == 8 && threads <= 256]);
+  const cudaError_t e = allow_smem(kernel, kSmem, done[NV == 8 && threads <= 256]);
   if (e != cudaSuccess) return e;
   const int sms = current_sms();
   if (!sms) return cudaErrorNoDevice;
@@ -550,11 +621,12 @@ cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_bwd(const ResNormGrad& a, int chunks, int groups, cudaStream_t s) {
   const int tpr = row_threads(a.f.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
-  const Ring ring = ring_of(a.f.D, R, {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
-  const int smem = std::max(ring.stages * ring.stage_bytes, R > 1 ? R * 3 * tpr * NV * 4 : 0);
+  const int coef = NV == 8 ? 0 : 2 * ((a.f.D + 7) / 8 * 8) * 4;
+  const Ring ring = ring_of(a.f.D, R, coef, {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
+  const int smem = std::max(ring.stages * ring.stage_bytes + coef, R > 1 ? R * 3 * tpr * NV * 4 : 0);
   auto* kernel = res_norm_grad_kernel<E, NV, RT, CT>;
   static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = allow_smem(kernel, kRingWide, done);
+  const cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_k(kernel, dim3((unsigned)chunks * groups), dim3(threads), smem, s, a, ring, chunks, tpr, R);
 }
@@ -566,11 +638,14 @@ cudaError_t by_form(bool vec, int D, bool res_f32, bool f32, F f) {
     return res_f32 ? f(e, nv, float{}, __nv_bfloat16{}) : f(e, nv, __nv_bfloat16{}, __nv_bfloat16{});
   };
   using std::integral_constant;
-  if (elems(D) == 8)
-    return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 8>{})
-               : types(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-  return vec ? types(integral_constant<int, 8>{}, integral_constant<int, 24>{})
-             : types(integral_constant<int, 1>{}, integral_constant<int, 24>{});
+  auto widths = [&](auto e) {
+    switch (elems(D)) {
+      case 8: return types(e, integral_constant<int, 8>{});
+      case 16: return types(e, integral_constant<int, 16>{});
+      default: return types(e, integral_constant<int, 24>{});
+    }
+  };
+  return vec ? widths(integral_constant<int, 8>{}) : widths(integral_constant<int, 1>{});
 }
 
 }  // namespace
