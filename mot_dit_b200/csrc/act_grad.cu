@@ -4,7 +4,8 @@
 // One pass over the saved pre-activations and the incoming gradient: the
 // product's operand dz (dg, du) is written once in the compute type, its
 // column sums are taken in fp32 before that rounding.  Bound by memory:
-// linear 3, gated 5 elements of traffic per output element.  A block owns 32 E
+// linear 3, gated 5 elements of traffic per output element (8448 x 4096 gated
+// bf16: 346 MB, 53 us at the copy rate).  A block owns 32 E
 // columns and one chunk of rows; eight row lanes keep their sums in registers
 // and join them in shared memory, in a fixed order, and the chunks are
 // added (in order) by the product that follows.
@@ -17,12 +18,17 @@ namespace wam {
 namespace {
 
 constexpr int kRows = 8;    // row lanes of a block
+constexpr int kBlocksPerSm = 4;
 
-// T: the compute type, DY: the incoming gradient's.
-template <int E, bool GATED, typename T, typename DY>
-__global__ void __launch_bounds__(32 * kRows, 4) act_grad_kernel(const ActGrad a) {
+// T: the compute type, DY: the incoming gradient's.  ANY: bf16 rows that do not
+// start on 16 bytes, eight elements at a time all the same (the written rows
+// are the workspace's, which do).
+template <int E, bool GATED, typename T, typename DY, bool ANY>
+__global__ void __launch_bounds__(32 * kRows, kBlocksPerSm) act_grad_kernel(const ActGrad a) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int kAhead = E == 1 ? 8 : E == 4 ? 4 : 2;  // rows a thread has in flight
+  // rows a thread has in flight (gated 8448 x 4096: 69 us with one, 82 with two
+  // and 76 at three blocks an SM; linear 48 us with two, 51 with one)
+  constexpr int kAhead = E == 1 ? 8 : E == 4 ? 4 : GATED ? 1 : 2;
   __shared__ float sh[GATED ? 2 : 1][kRows][32 * E];
   const int tx = threadIdx.x, ty = threadIdx.y;
   const int n = (blockIdx.x * 32 + tx) * E, chunk = blockIdx.y;
@@ -44,9 +50,15 @@ __global__ void __launch_bounds__(32 * kRows, 4) act_grad_kernel(const ActGrad a
         const int r = r0 + i * kRows;
         if (r < hi) {
           const size_t at = (size_t)r * a.N + n;
-          rd[i].load(dy + at);
-          if (pz) rz[i].load(pz + at);
-          if (GATED) ru[i].load(pu + at);
+          if constexpr (ANY) {
+            rd[i].v = fetch8(OpMat{a.dy, a.N, a.N, a.M}, r, n);
+            if (pz) rz[i].v = fetch8(OpMat{a.z, a.N, a.N, a.M}, r, n);
+            if (GATED) ru[i].v = fetch8(OpMat{a.u, a.N, a.N, a.M}, r, n);
+          } else {
+            rd[i].load(dy + at);
+            if (pz) rz[i].load(pz + at);
+            if (GATED) ru[i].load(pu + at);
+          }
         }
       }
 #pragma unroll
@@ -96,10 +108,10 @@ __global__ void __launch_bounds__(32 * kRows, 4) act_grad_kernel(const ActGrad a
   }
 }
 
-template <int E, bool GATED, typename T, typename DY>
+template <int E, bool GATED, typename T, typename DY, bool ANY = false>
 cudaError_t run(const ActGrad& a, cudaStream_t s) {
   const dim3 grid((a.N + 32 * E - 1) / (32 * E), a.chunks);
-  return launch_k(act_grad_kernel<E, GATED, T, DY>, grid, dim3(32, kRows), 0, s, a);
+  return launch_k(act_grad_kernel<E, GATED, T, DY, ANY>, grid, dim3(32, kRows), 0, s, a);
 }
 template <int E, typename T>
 cudaError_t run_types(const ActGrad& a, cudaStream_t s) {
@@ -138,7 +150,7 @@ cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s) {
 // Two full waves of blocks at four an SM, chunks of at least 16 rows, and no
 // more than 128 (their sums are added one after another).
 int act_grad_chunks(int M, int N, bool f32) {
-  const int e = f32 ? (N % 4 ? 1 : 4) : (N % 8 ? 1 : 8), cols = (N + 32 * e - 1) / (32 * e);
+  const int e = f32 ? (N % 4 ? 1 : 4) : 8, cols = (N + 32 * e - 1) / (32 * e);
   return std::max(1, std::min({(1184 + cols - 1) / cols, (M + 15) / 16, 128}));
 }
 
@@ -147,7 +159,10 @@ cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {
   const bool ptrs = al(a.dy) && al(a.z) && al(a.u) && al(a.dz) && al(a.du);
   if (a.f32)
     return ptrs && a.N % 4 == 0 && a.ld_dz % 4 == 0 ? run_types<4, float>(a, s) : run_types<1, float>(a, s);
-  return ptrs && a.N % 8 == 0 && a.ld_dz % 8 == 0 ? run_types<8, __nv_bfloat16>(a, s) : run_types<1, __nv_bfloat16>(a, s);
+  using H = __nv_bfloat16;
+  if (ptrs && a.N % 8 == 0 && a.ld_dz % 8 == 0) return run_types<8, H>(a, s);
+  if (a.dy_f32) return run<1, false, H, float>(a, s);
+  return a.u ? run<8, true, H, H, true>(a, s) : run<8, false, H, H, true>(a, s);
 }
 
 cudaError_t launch_repack(const void* src, void* dst, int rows, int cols, int ld, cudaStream_t s) {

@@ -614,7 +614,7 @@ cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const int sms = current_sms();
   if (!sms) return cudaErrorNoDevice;
   // as many blocks as run at once: by registers (see the launch bounds) and by shared memory
-  const int per = std::min(threads > 256 ? 1 : NV == 8 ? (E == 8 ? 3 : 2) : 1, 227 * 1024 / (smem + 3072));
+  const int per = std::min(threads > 256 ? 1 : NV == 8 ? (E == 8 ? 3 : 2) : 1, 227 * 1024 / (smem + 3 * 1024));
   const int grid = std::max(1, std::min((a.M + R - 1) / R, sms * std::max(1, per)));
   return launch_k(kernel, dim3(grid), dim3(threads), smem, s, a, ring, tpr, R);
 }

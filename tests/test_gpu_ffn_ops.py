@@ -322,3 +322,196 @@ def test_residual_norm_backward(M, per, D, r, t, post, gate, mod, gain, alpha):
     W.op_residual_norm_backward(CODE[t], s, y, None, dh, a, b, M, D, **kw)
     W.op_residual_norm_backward(CODE[t], s, y, zero, dh, a2, b2, M, D, **kw)
     assert torch.equal(a, a2) and torch.equal(b, b2)
+
+
+# ----------------------------------------------------------- more of each
+@pytest.mark.parametrize("M,N,K,o,res", [
+    (300, 200, 2000, FP, True),    # a segmented reduction, ragged
+    (1088, 384, 6144, FP, True),   # seven segments
+    (2600, 1100, 1000, FP, False),  # two segments on CTA pairs
+    (32, 500, 1537, FP, True),     # segments behind the loader warps
+    (16, 4200, 520, BF, True),     # few tokens, two feature groups a block
+    (2, 640, 6144, FP, False),     # few tokens, a group shared by a cluster
+    (9, 100, 333, BF, True),       # few tokens, rows at any alignment
+])
+def test_linear_forms(M, N, K, o, res):
+    n = T.normals(M + N + K)
+    x, w, b = n(M, K, dtype=BF), n(N, K, std=K ** -0.5, dtype=BF), n(N)
+    r = n(M, N, dtype=o) if res else None
+    y, ok = T.guarded((M, N), o)
+    W.op_linear_act(W.BF16, x, w, b, y, M, N, K, residual=r, out_dtype=CODE[o])
+    _, _, y64, ey = T.linear64(x, w, b, r, "none", o)
+    T.within(y, y64, ey)
+    ok()
+    if o == FP:  # the accumulation's truncations stay near fp32's own roundings
+        assert ((y.double() - y64).norm() / y64.norm()).item() < 1e-6
+
+
+def test_fp32_products_are_fp32():
+    """Three parts an operand: the sums are as near as an fp32 matrix product's, at any scale of the operands."""
+    M, N, K = 200, 300, 1500
+    n = T.normals(5)
+    for scale in (1.0, 1e-20, 1e15):
+        x, w = n(M, K, std=scale), n(N, K, std=1 / scale)
+        y = torch.empty(M, N, device="cuda")
+        W.op_linear_act(W.FP32, x, w, None, y, M, N, K)
+        want = x.double() @ w.double().t()
+        assert ((y.double() - want).norm() / want.norm()).item() < 1e-6
+
+
+@pytest.mark.parametrize("t", [BF, FP])
+def test_linear_special_values(t):
+    """A row with a NaN or an infinity spoils itself only; infinite pre-activations have their limits."""
+    M, N, K = 140, 64, 96
+    n = T.normals(3)
+    x, w = n(M, K, dtype=t), n(N, K, dtype=t)
+    clean = torch.empty(M, N, dtype=t, device="cuda")
+    W.op_linear_act(CODE[t], x, w, None, clean, M, N, K, act=ACT["silu"])
+    x[7, 3], x[90, 5] = float("nan"), float("inf")
+    y = torch.empty_like(clean)
+    W.op_linear_act(CODE[t], x, w, None, y, M, N, K, act=ACT["silu"])
+    bad = ~torch.isfinite(y)
+    assert torch.isnan(y[7]).all() and bad[90].any()
+    keep = [i for i in range(M) if i not in (7, 90)]
+    assert torch.equal(y[keep], clean[keep])
+    z = torch.tensor([[float("inf"), float("-inf"), 1e30, -1e30, 0.0, -0.0, 100.0, -100.0]], device="cuda").to(t)
+    z = torch.nn.functional.pad(z, (0, 56))
+    dy = torch.ones(1, N, dtype=t, device="cuda")
+    for name, limit in (("silu", [1, 0, 1, 0]), ("gelu_tanh", [1, 0, 1, 0]), ("gelu_erf", [1, 0, 1, 0]), ("sigmoid", [0, 0, 0, 0]),
+                        ("relu", [1, 0, 1, 0])):
+        db = torch.empty(N, device="cuda")
+        ws = _ws(W.op_linear_act_workspace(CODE[t], 1, N, K, act=ACT[name]))
+        W.op_linear_act_backward(CODE[t], None, None, z, dy, None, None, db, 1, N, K, act=ACT[name], workspace=ws)
+        assert torch.isfinite(db).all() and db[:4].tolist() == limit, (name, db[:4])
+
+
+@pytest.mark.parametrize("act", W.ACTS)
+def test_gradients_against_differences(act):
+    """fp32: central differences of the forward operators themselves."""
+    M, N, K = 6, 24, 32
+    n = T.normals(11)
+    x, w, b, dy = n(M, K), n(N, K, std=K ** -0.5), n(N, std=0.3), n(M, N)
+    if act == "relu":  # (no pre-activation within a step of the corner)
+        b = b + 0.0
+    run = lambda x_, w_: (W.op_linear_act(W.FP32, x_, w_, b, y, M, N, K, act=ACT[act], z=z), (y.double() * dy.double()).sum().item())[1]  # noqa: E731
+    y, z = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    run(x, w)
+    z0 = z.clone()
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    W.op_linear_act_backward(W.FP32, x, w, z0, dy, dx, dw, db, M, N, K, act=ACT[act],
+                             workspace=_ws(W.op_linear_act_workspace(W.FP32, M, N, K, act=ACT[act])))
+    h = 2.0 ** -7
+    for (src, grad, at) in ((x, dx, (2, 5)), (x, dx, (5, 31)), (w, dw, (3, 7)), (w, dw, (23, 0))):
+        lo, hi = src.clone(), src.clone()
+        lo[at] -= h
+        hi[at] += h
+        if act == "relu":
+            run(hi if src is x else x, hi if src is w else w)
+            z1 = z.clone()
+            run(lo if src is x else x, lo if src is w else w)
+            if ((z1 > 0) != (z > 0)).any():  # a corner between the two points: no difference quotient
+                continue
+        diff = (run(hi if src is x else x, hi if src is w else w) - run(lo if src is x else x, lo if src is w else w)) / (2 * h)
+        # third derivatives times h^2 / 6 of up to N terms, and fp32 rounding over 2 h
+        assert abs(diff - grad[at].item()) < 1e-3 * (1 + abs(diff)), (act, at, diff, grad[at].item())
+
+
+def test_zero_rows():
+    n = T.normals(1)
+    w = n(24, 32, dtype=BF)
+    e = torch.empty(0, 32, dtype=BF, device="cuda")
+    o = torch.empty(0, 24, dtype=BF, device="cuda")
+    W.op_linear_act(W.BF16, e, w, None, o, 0, 24, 32)
+    W.op_gated(W.BF16, e, w, w, o, 0, 24, 32)
+    dw, db = torch.full((24, 32), 5.0, dtype=BF, device="cuda"), torch.full((24,), 5.0, device="cuda")
+    W.op_linear_act_backward(W.BF16, e, w, o, o, e.clone(), dw, db, 0, 24, 32, act=2)
+    assert not dw.any() and not db.any()
+    d2, d3, b2, b3 = torch.ones_like(dw), torch.ones_like(dw), torch.ones_like(db), torch.ones_like(db)
+    W.op_gated_backward(W.BF16, e, w, w, o, o, o, e.clone(), d2, d3, 0, 24, 32, dbias_g=b2, dbias_u=b3)
+    assert not d2.any() and not d3.any() and not b2.any() and not b3.any()
+    g = torch.ones(32, device="cuda")
+    z = torch.empty(0, 32, device="cuda")
+    W.op_residual_norm(W.BF16, z, e, z.clone(), e.clone(), 0, 32)
+    W.op_residual_norm_backward(W.BF16, z, e, z, e, z.clone(), e.clone(), 0, 32, post_norm=True, dpost_gain=g)
+    assert not g.any()
+
+
+def _block(stream, s, M=70, D=264, F=520, G=2):
+    """A feed-forward half of a block, forward and backward, with the operators alone; s: its buffers."""
+    per = -(-M // G)
+    kw = dict(stream=stream)
+    W.op_gated(W.BF16, s["h"], s["wg"], s["wu"], s["a"], M, F, D, g=s["g"], u=s["u"], **kw)
+    W.op_linear_act(W.BF16, s["a"], s["wd"], s["bd"], s["y"], M, D, F, **kw)
+    mod = dict(post_norm=True, post_gain=s["pg"], gate=s["table"][:, 0], gain=s["gain"], scale=s["table"][:, 1], rows_per_group=per,
+               ld_mod=3 * D)
+    W.op_residual_norm(W.BF16, s["x"], s["y"], s["s"], s["h2"], M, D, shift=s["table"][:, 2], **mod, **kw)
+    W.op_residual_norm_backward(W.BF16, s["s"], s["y"], s["ds"], s["dh2"], s["dx"], s["dy"], M, D, dpost_gain=s["dpg"], dgate=s["dgate"],
+                                dgain=s["dgain"], dscale=s["dscale"], dshift=s["dshift"], workspace=s["ws1"], **mod, **kw)
+    W.op_linear_act_backward(W.BF16, s["a"], s["wd"], None, s["dy"], s["da"], s["dwd"], s["dbd"], M, D, F, workspace=s["ws2"], **kw)
+    W.op_gated_backward(W.BF16, s["h"], s["wg"], s["wu"], s["g"], s["u"], s["da"], s["dh"], s["dwg"], s["dwu"], M, F, D,
+                        workspace=s["ws3"], **kw)
+
+
+def _block_state(seed, M=70, D=264, F=520, G=2):
+    n = T.normals(seed)
+    b = lambda *sh: torch.full(sh, float("nan"), dtype=BF, device="cuda")  # noqa: E731
+    f = lambda *sh: torch.full(sh, float("nan"), device="cuda")  # noqa: E731
+    return dict(h=n(M, D, dtype=BF), x=n(M, D), wg=n(F, D, std=D ** -0.5, dtype=BF), wu=n(F, D, std=D ** -0.5, dtype=BF),
+                wd=n(D, F, std=F ** -0.5, dtype=BF), bd=n(D, std=0.1), pg=n(D, mean=1.0, std=0.1), gain=n(D, mean=1.0, std=0.1),
+                table=n(G, 3, D, std=0.5), ds=n(M, D), dh2=n(M, D, dtype=BF), a=b(M, F), g=b(M, F), u=b(M, F), y=b(M, D), s=f(M, D),
+                h2=b(M, D), dx=f(M, D), dy=b(M, D), dpg=f(D), dgate=f(G, D), dgain=f(D), dscale=f(G, D), dshift=f(G, D), da=b(M, F),
+                dwd=b(D, F), dbd=f(D), dh=b(M, D), dwg=b(F, D), dwu=b(F, D), ws1=_ws(W.op_residual_norm_workspace(M, D, -(-M // G))),
+                ws2=_ws(W.op_linear_act_workspace(W.BF16, M, D, F)), ws3=_ws(W.op_gated_workspace(W.BF16, M, F, D)))
+
+
+def test_block_against_autograd():
+    """The operators together against the definition's gradient in 64 bits.  Every stage rounds to bf16 once or twice
+    (2^-8 each); eight such roundings lie on the longest way, and errors pass through factors of about one."""
+    M, D, G = 70, 264, 2
+    s = _block_state(0)
+    _block(None, s)
+    leaf = {k: s[k].double().requires_grad_() for k in ("h", "x", "wg", "wu", "wd", "bd", "pg", "gain", "table")}
+    a = torch.nn.functional.silu(leaf["h"] @ leaf["wg"].t()) * (leaf["h"] @ leaf["wu"].t())
+    y = a @ leaf["wd"].t() + leaf["bd"]
+    tb = leaf["table"]
+    st, h2 = T.norm64(leaf["x"], y, True, leaf["pg"], tb[:, 0], leaf["gain"], tb[:, 1], tb[:, 2], 1.0, M // G)
+    grads = dict(zip(leaf, torch.autograd.grad([st, h2], list(leaf.values()), [s["ds"].double(), s["dh2"].double()])))
+    got = dict(h="dh", x="dx", wg="dwg", wu="dwu", wd="dwd", bd="dbd", pg="dpg", gain="dgain")
+    pairs = [(s["s"], st), (s["h2"], h2)] + [(s[v], grads[k]) for k, v in got.items()]
+    pairs += [(s[k], grads["table"][:, i]) for i, k in enumerate(("dgate", "dscale", "dshift"))]
+    for x, want in pairs:
+        assert torch.isfinite(x).all()
+        assert ((x.double() - want).norm() / want.norm()).item() < 8 * 2.0 ** -8
+
+
+def test_block_captured_and_on_streams():
+    """A captured block replays to the eager bits with new inputs; two streams with their own workspaces do not disturb
+    each other; tensors made on one stream are used on another."""
+    keys = ("s", "h2", "dx", "dy", "dpg", "dgate", "dgain", "dscale", "dshift", "dwd", "dbd", "dh", "dwg", "dwu")
+    want = {}
+    for seed in (1, 2):
+        s = _block_state(seed)
+        _block(None, s)
+        want[seed] = {k: s[k].clone() for k in keys}
+    s = _block_state(1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _block(torch.cuda.current_stream(), s)
+    for seed in (2, 1, 2):
+        new = _block_state(seed)
+        for k in ("h", "x", "wg", "wu", "wd", "bd", "pg", "gain", "table", "ds", "dh2"):
+            s[k].copy_(new[k])
+        g.replay()
+        torch.cuda.synchronize()
+        for k in keys:
+            assert torch.equal(s[k], want[seed][k]), (seed, k)
+    s1, s2 = _block_state(1), _block_state(2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    a.wait_stream(torch.cuda.current_stream()), b.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        _block(a, s1)
+        _block(b, s2)
+    torch.cuda.synchronize()
+    for k in keys:
+        assert torch.equal(s1[k], want[1][k]) and torch.equal(s2[k], want[2][k]), k
