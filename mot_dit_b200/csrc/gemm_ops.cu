@@ -974,7 +974,8 @@ constexpr int kChainF32 = 12;  // fp32 operands: 768
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Accumulator columns of product p's tiles under plan width bn.
 int tile_cols(const OpProduct& p, const Plan& pl) {
-  const int q = pl.cg == 2 ? 128 : 64;  // (MN-major halves of a pair are whole 64-column boxes)
+  // (an MN-major operand comes in boxes of 64 columns, in halves to a pair; a gated tile's halves in 32s)
+  const int q = pl.cg == 2 ? 128 : p.b_mn || p.gated ? 64 : 32;
   const int n = p.gated ? 2 * ceil_div(p.N, 32) * 32 : p.N;
   return std::min(pl.bn, ceil_div(n, q) * q);
 }
@@ -983,7 +984,9 @@ int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, B
 // Estimated ns of a plan, from measured parts: one k-block of a tile (all SMs
 // busy, operands from L2), what follows a tile's last MMA, and the launch.
 double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int mode) {
-  const double per = mode == kF32 ? (pl.bn == 128 ? 950 : 700) : pl.cg == 2 ? (pl.bn == 256 ? 370 : 270) : pl.bn == 256 ? 410 : pl.bn == 128 ? 250 : 180;
+  const double per = mode == kF32 ? (pl.bn == 128 ? 950 : 700)
+                     : pl.cg == 2 ? 170 + 0.78 * pl.bn
+                     : pl.bn <= 128 ? 110 + 1.1 * pl.bn : 90 + 1.25 * pl.bn;
   const double tail = 11.0 * pl.bn + 600;
   if (pl.split > 1) {
     const OpProduct& q = p[0];
@@ -1034,7 +1037,7 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
   auto consider = [&](Plan pl) {
     pl.seg = std::max(1, ceil_div(ceil_div(chain, pl.split), mode == kF32 ? kChainF32 : kChain));
     if (mode != kF32) {
-      if (pl.seg > 1 && pl.bn > 128) return;  // (two buffers and the sums: no tensor memory for wider tiles)
+      if (pl.seg > 1 && pl.bn > 160) return;  // (two buffers and the sums: no tensor memory for wider tiles)
     } else if (pl.seg > 512 / pl.bn - 1) {  // no tensor memory for so many: the narrowest tile takes what there is
       if (pl.bn > 64) return;
       pl.seg = 512 / pl.bn - 1;
@@ -1042,15 +1045,23 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
     const double c = plan_cost(p, n, pl, d, mode);
     if (c < bc) bc = c, best = pl;
   };
-  for (int bn : {256, 128, 64}) {
-    if (mode == kF32 && bn == 256) continue;  // (six parts of a 256-wide tile leave no second stage)
+  // Widths between the powers of two fill the SMs more evenly (1088 x 1536: 144
+  // tiles of 96 columns, 31.6 us; 108 of 128, 33.8 us).  A reduction-outermost
+  // operand takes a load per 64 columns, and they lose there (2049 x 4111 x 1544
+  // backward: 192 wide 111 us, pairs 83 us).
+  const bool narrow = n == 1 && !p[0].gated && !p[0].b_mn;
+  for (int bn = mode == kF32 ? 128 : 256; bn >= 64; bn -= 32) {  // (fp32: six parts of a wider tile leave no second stage)
+    if ((bn & (bn - 1)) && (!narrow || mode == kF32)) continue;
     consider(Plan{1, bn, 1, 1});
-    if (n == 1)
-      for (int s = 2; s <= 8; ++s)
-        if (k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s, 1});
+    if (n > 1) continue;
+    const int cols = tile_cols(p[0], Plan{1, bn, 1, 1});
+    const long long tiles = (long long)ceil_div(p[0].M, BM) * ceil_div(p[0].gated ? 2 * p[0].N : p[0].N, cols);
+    for (int s = 2; s <= 8; ++s)
+      if (tiles <= d.clusters[s] && k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s, 1});
   }
   if (mode == kTma) {
     consider(Plan{2, 256, 1, 1});
+    if (narrow) consider(Plan{2, 192, 1, 1});  // (halves of 96 columns)
     consider(Plan{2, 128, 1, 1});
   }
   return best;
