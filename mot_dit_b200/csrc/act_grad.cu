@@ -151,7 +151,7 @@ cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s) {
 // more than 128 (their sums are added one after another).
 int act_grad_chunks(int M, int N, bool f32) {
   const int e = f32 ? (N % 4 ? 1 : 4) : 8, cols = (N + 32 * e - 1) / (32 * e);
-  return std::max(1, std::min({(1184 + cols - 1) / cols, (M + 15) / 16, 128}));
+  return std::max(1, std::min({1184 / cols, (M + 15) / 16, 128}));
 }
 
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s) {

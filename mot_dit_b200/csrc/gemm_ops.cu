@@ -74,7 +74,7 @@ struct GemmArgs {
   OpColSum sums[2];
   int np, n_sums, tiles;
   int stages, stage_bytes;
-  int subs, sub_bytes;  // k-blocks of a full stage, and the bytes of one
+  int subs;  // k-blocks of a full stage
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
   int nbuf, buf_cols;  // accumulator buffers
   int nseg;            // segments of a tile's reduction
@@ -135,13 +135,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn) {
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn, int subs) {
   // K-major: rows of 64 reduction elements, 8-row groups 1024 B apart.
   // MN-major: rows of 64 output elements, one row per reduction index; 8-row
   // groups 1024 B apart along the reduction (stride offset), blocks of 64
-  // output elements 8192 B apart (leading offset).
+  // output elements a stage's 64 subs rows apart (leading offset).
   uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(mn ? (8192 >> 4) : 1) << 16;
+  d |= static_cast<uint64_t>(mn ? (subs * 8192) >> 4 : 1) << 16;
   d |= static_cast<uint64_t>(1024 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const int brows = P.bn / CG;
         const bool gated = P.gated, amn = P.a_mn, bmn = P.b_mn;
         const int n0 = gated ? tl.n * (P.bn / 2) : tl.n * P.bn + (CG == 2 ? (int)rank * brows : 0);
-        const uint32_t bytes = (uint32_t)(kABytes + brows * BK * 2) * CG;
+        const int bbytes = brows * BK * 2, subs = g.subs;
         const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0;
         for (int q = 0; q < 2 && ok; ++q) {  // operand pairs
           const CUtensorMap* ma = &P.ma[q];
@@ -505,9 +505,12 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
               ok = false;
               break;
             }
-            const int ns = min(g.subs, end - kb);
-            if (!peer) mbar_arrive_expect_tx(&full[st], bytes * ns);
+            const int ns = min(subs, end - kb);
+            // (a reduction-outermost box brings the rows of a whole stage)
+            if (!peer)
+              mbar_arrive_expect_tx(&full[st], (uint32_t)(kABytes * (amn ? subs : ns) + bbytes * (bmn ? subs : ns)) * CG);
             uint8_t* sa = smem + (size_t)st * sbytes;
+            uint8_t* sb = sa + subs * kABytes;
             const uint32_t bar = full0 + 8 * st;
             auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
               if (CG == 2)
@@ -515,22 +518,22 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
               else
                 tma_load_3d(dst, map, &full[st], x, y, 0);
             };
-            for (int i = 0; i < ns; ++i, ++kb, sa += g.sub_bytes) {
-              const int kk = (q ? kb - kb0 : kb) * BK;
-              uint8_t* sb = sa + kABytes;
-              if (amn) {
-                load(ma, sa, m0, kk);
-                load(ma, sa + 8192, m0 + 64, kk);
-              } else {
-                load(ma, sa, kk, m0);
-              }
-              if (bmn) {
-                for (int j = 0; j < brows; j += 64) load(mb, sb + j * 128, n0 + j, kk);
-              } else {
-                load(mb, sb, kk, n0);  // gated: g's rows, then u's (a pair: one CTA each)
-                if (CG == 1 && gated) load(mb1, sb + brows / 2 * 128, kk, n0);
+            const int k0 = (q ? kb - kb0 : kb) * BK;
+            if (amn) {
+              load(ma, sa, m0, k0);
+              load(ma, sa + subs * 8192, m0 + 64, k0);
+            } else {
+              for (int i = 0; i < ns; ++i) load(ma, sa + i * kABytes, k0 + i * BK, m0);
+            }
+            if (bmn) {
+              for (int j = 0; j < brows; j += 64) load(mb, sb + subs * j * 128, n0 + j, k0);
+            } else {
+              for (int i = 0; i < ns; ++i) {
+                load(mb, sb + i * bbytes, k0 + i * BK, n0);  // gated: g's rows, then u's (a pair: one CTA each)
+                if (CG == 1 && gated) load(mb1, sb + i * bbytes + bbytes / 2, k0 + i * BK, n0);
               }
             }
+            kb += ns;
             if (++st == stages) st = 0, phase ^= 1;
           }
         }
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
     }
   } else if (warp == 1) {
     if (rank * (CG - 1) == 0 && elect_one()) {
-      const int subs = g.subs, sub_bytes = g.sub_bytes;
+      const int subs = g.subs;
       const uint32_t smem0 = smem_u32(smem);
       int st = 0, buf = 0, lt = 0;
       uint32_t phase = 0, bphase = 0;
@@ -561,7 +564,9 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const uint32_t bn = P.bn;
         const uint32_t idesc = idesc_bf16_f32(BM * CG, bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
         const uint64_t sa = amn ? 2048 >> 4 : 32 >> 4, sb = bmn ? 2048 >> 4 : 32 >> 4;  // descriptor step per K = 16
-        const uint64_t da0 = smem_desc(0, amn), db0 = smem_desc(0, bmn);
+        const uint64_t da0 = smem_desc(0, amn, subs), db0 = smem_desc(0, bmn, subs);
+        // bytes from one k-block of a stage to the next
+        const uint32_t a_sub = amn ? 8192 : kABytes, b_sub = bmn ? 8192 : bn / CG * BK * 2;
         const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0, seg = seg_blocks(hi - lo);
         uint32_t d = tmem + buf * buf_cols;
         int in = 0;  // k-blocks in the present segment
@@ -599,10 +604,10 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
             ++in, ++kb;
           } else {
           const int ns = min(subs, (kb < kb0 ? min(hi, kb0) : hi) - kb);  // (a stage never spans two operand pairs)
-          uint32_t a0 = smem0 + (uint32_t)(st * sbytes);
-          for (int i = 0; i < ns; ++i, ++kb, a0 += sub_bytes) {
+          uint32_t a0 = smem0 + (uint32_t)(st * sbytes), b0 = a0 + subs * kABytes;
+          for (int i = 0; i < ns; ++i, ++kb, a0 += a_sub, b0 += b_sub) {
             // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
-            const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | ((a0 + kABytes) >> 4 & 0x3FFF);
+            const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | (b0 >> 4 & 0x3FFF);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
               const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
@@ -984,15 +989,20 @@ int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, B
 // Estimated ns of a plan, from measured parts: one k-block of a tile (all SMs
 // busy, operands from L2), what follows a tile's last MMA, and the launch.
 double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int mode) {
-  const double per = mode == kF32 ? (pl.bn == 128 ? 950 : 700)
-                     : pl.cg == 2 ? 170 + 0.78 * pl.bn
-                     : pl.bn <= 128 ? 110 + 1.1 * pl.bn : 90 + 1.25 * pl.bn;
-  const double tail = 11.0 * pl.bn + 600;
+  // a k-block: the tensor core and its operands, or the issue of its loads (115 ns each)
+  auto per = [&](const OpProduct& q) {
+    if (mode == kF32) return pl.bn == 128 ? 950.0 : 700.0;
+    const double base = pl.cg == 2 ? 170 + 0.78 * pl.bn : pl.bn <= 128 ? 110 + 1.1 * pl.bn : 90 + 1.25 * pl.bn;
+    const double subs = pl.bn / pl.cg <= 128 ? 2 : 1;
+    const double loads = (q.a_mn ? 2 / subs : 1) + (q.b_mn ? pl.bn / pl.cg / 64 / subs : q.gated && pl.cg == 1 ? 2 : 1);
+    return std::max(base, 115 * loads);
+  };
+  const double tail = 11.0 * pl.bn + 600 + (pl.cg == 2 ? 1000 : 0);
   if (pl.split > 1) {
     const OpProduct& q = p[0];
     const int bn = tile_cols(q, pl), tn = ceil_div(q.gated ? 2 * q.N : q.N, bn), tm = ceil_div(q.M, BM);
     const int waves = ceil_div(tm * tn, d.clusters[pl.split]);
-    return waves * (ceil_div(k_blocks(q), pl.split) * per + tail + 2500);
+    return waves * (ceil_div(k_blocks(q), pl.split) * per(q) + tail + 2500);
   }
   const int units = pl.cg == 2 ? d.clusters[2] : d.sms;
   const bool bare = mode == kF32;  // one accumulator buffer: every tile's epilogue stands alone
@@ -1000,7 +1010,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   if (n == 1) {
     const int bn = tile_cols(p[0], pl), cols = p[0].gated ? 2 * p[0].N : p[0].N;
     const long long tiles = (long long)ceil_div(p[0].M, BM * pl.cg) * ceil_div(cols, bn);
-    return (double)((tiles + units - 1) / units) * (k_blocks(p[0]) * per + extra) + tail;
+    return (double)((tiles + units - 1) / units) * (k_blocks(p[0]) * per(p[0]) + extra) + tail;
   }
   // several products: the busiest unit's tiles
   double worst = 0;
@@ -1010,7 +1020,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   for (int i = 0; i < n; ++i) {
     const long long tiles = (long long)ceil_div(p[i].M, BM * pl.cg) *
                             ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl));
-    c[i] = k_blocks(p[i]) * per + extra;
+    c[i] = k_blocks(p[i]) * per(p[i]) + extra;
     first[i] = (int)(pos % units);
     whole[i] = tiles / units;
     rest[i] = tiles % units;
@@ -1092,10 +1102,16 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
   }
   const Plan pl = choose(p, n, mode, *d);
   GemmArgs g;
+  int bmax = 0;
+  for (int i = 0; i < n; ++i) bmax = std::max(bmax, tile_cols(p[i], pl));
+  const int sub_bytes = (kABytes + bmax / pl.cg * BK * 2) * (f32 ? 3 : 1), room = kSmemMax - kBarBytes - kEpiWarps * kStg;
+  g.subs = mode == kTma && 6 * sub_bytes <= room ? 2 : 1;
+  g.stage_bytes = g.subs * sub_bytes;
+  g.stages = std::min(kMaxStages, room / g.stage_bytes);
   g.np = n;
   g.n_sums = n_sums;
   for (int i = 0; i < n_sums; ++i) g.sums[i] = sums[i];
-  int tiles = 0, bmax = 0;
+  int tiles = 0;
   for (int i = 0; i < n; ++i) {
     const OpProduct& q = p[i];
     ProductK& k = g.p[i];
@@ -1112,25 +1128,20 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
     k.b_mn = q.b_mn;
     k.gated = q.gated;
     k.e = q.e;
-    bmax = std::max(bmax, k.bn);
     for (int j = 0; j < 2; ++j) {
       const OpMat& ma = q.a[q.pairs == 2 ? j : 0];
       const OpMat& mb = q.b[(q.pairs == 2 || q.gated) ? j : 0];
       k.a[j] = ma;
       k.b[j] = mb;
       if (mode != kTma) continue;
-      const int boxb = q.b_mn ? 64 : q.gated ? k.bn / 2 : k.bn / pl.cg;
-      if (!make_tmap_rows(&k.ma[j], ma.p, ma.inner, ma.outer, ma.ld, q.a_mn ? 64 : BM) ||
+      const int boxb = q.b_mn ? 64 * g.subs : q.gated ? k.bn / 2 : k.bn / pl.cg;
+      if (!make_tmap_rows(&k.ma[j], ma.p, ma.inner, ma.outer, ma.ld, q.a_mn ? 64 * g.subs : BM) ||
           !make_tmap_rows(&k.mb[j], mb.p, mb.inner, mb.outer, mb.ld, boxb))
         return cudaErrorInvalidValue;
     }
   }
   g.tiles = tiles;
   g.split = pl.split;
-  g.sub_bytes = (kABytes + bmax / pl.cg * BK * 2) * (f32 ? 3 : 1);
-  g.subs = mode == kTma && 6 * g.sub_bytes <= kSmemMax - kBarBytes - kEpiWarps * kStg ? 2 : 1;
-  g.stage_bytes = g.subs * g.sub_bytes;
-  g.stages = std::min(kMaxStages, (kSmemMax - kBarBytes - kEpiWarps * kStg) / g.stage_bytes);
   g.nseg = pl.seg;
   g.nbuf = f32 ? 1 : 2;
   g.tm_cols = 32;
