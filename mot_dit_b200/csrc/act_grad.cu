@@ -129,6 +129,33 @@ __global__ void __launch_bounds__(256) repack_kernel(const OpMat src, __nv_bfloa
   }
 }
 
+struct PartSums {
+  OpPartSum s[kOpProducts];
+};
+__global__ void __launch_bounds__(256) part_sum_kernel(const PartSums a) {
+  pdl_trigger();
+  pdl_wait();
+  const OpPartSum& s = a.s[blockIdx.y];
+  const bool vec = s.n % 4 == 0 && (reinterpret_cast<uintptr_t>(s.out) & 15) == 0;
+  const int e = vec ? 4 : 1;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * e; i < s.n; i += (size_t)gridDim.x * 256 * e) {
+    if (vec) {
+      float4 v = *reinterpret_cast<const float4*>(s.part + i);
+#pragma unroll 4
+      for (int p = 1; p < s.pieces; ++p) {
+        const float4 x = *reinterpret_cast<const float4*>(s.part + p * s.n + i);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      const float o[4] = {v.x, v.y, v.z, v.w};
+      store_any<4>(s.out, s.f32, i, o);
+    } else {
+      float o[1] = {0.f};
+#pragma unroll 4
+      for (int p = 0; p < s.pieces; ++p) o[0] += s.part[p * s.n + i];
+      store_any<1>(s.out, s.f32, i, o);
+    }
+  }
+}
 __global__ void __launch_bounds__(128) col_sum_kernel(const OpColSum a, const OpColSum b) {
   pdl_trigger();
   pdl_wait();
@@ -142,6 +169,16 @@ __global__ void __launch_bounds__(128) col_sum_kernel(const OpColSum a, const Op
 }
 
 }  // namespace
+
+cudaError_t launch_part_sums(const OpPartSum* sums, int n, cudaStream_t s) {
+  PartSums a{};
+  size_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    a.s[i] = sums[i];
+    most = std::max(most, sums[i].n);
+  }
+  return launch_k(part_sum_kernel, dim3((unsigned)std::min<size_t>((most + 1023) / 1024, 148 * 8), n), dim3(256), 0, s, a);
+}
 
 cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s) {
   return launch_k(col_sum_kernel, dim3((sums[0].cols + 127) / 128, n), dim3(128), 0, s, sums[0], sums[n - 1]);

@@ -64,6 +64,7 @@ struct ProductK {
   OpMat a[2], b[2];
   int M, N;           // N: columns of the output (gated: of g and of u each)
   int kb0, kb;        // k-blocks of the first operand pair, of all pairs
+  int pieces;         // shares of the reduction, each a tile of its own with its own output
   int bn;             // accumulator columns of a tile (gated: g and u halves)
   int tiles_m, tiles_n, tile0;
   int a_mn, b_mn, gated;
@@ -83,13 +84,21 @@ struct GemmArgs {
 
 struct Tile {
   int p, m, n;  // product, row tile, column tile
+  int piece;
 };
 __device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t) {
   Tile r;
   r.p = 0;
   while (r.p + 1 < g.np && t >= g.p[r.p + 1].tile0) ++r.p;
   const ProductK& P = g.p[r.p];
-  const int l = t - P.tile0, per = kRaster * P.tiles_n, grp = l / per, in = l - grp * per;
+  int l = t - P.tile0;
+  r.piece = 0;
+  if (P.pieces > 1) {
+    const int plane = P.tiles_m * P.tiles_n;
+    r.piece = l / plane;
+    l -= r.piece * plane;
+  }
+  const int per = kRaster * P.tiles_n, grp = l / per, in = l - grp * per;
   const int gm = min(kRaster, P.tiles_m - grp * kRaster);
   r.m = grp * kRaster + in % gm;
   r.n = in / gm;
@@ -472,8 +481,12 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
   pdl_trigger();
 
   // k-blocks of this CTA's part of a tile
-  auto k_lo = [&](const ProductK& P) { return S > 1 ? (int)((long long)P.kb * rank / S) : 0; };
-  auto k_hi = [&](const ProductK& P) { return S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : P.kb; };
+  auto k_lo = [&](const ProductK& P, int piece) {
+    return S > 1 ? (int)((long long)P.kb * rank / S) : (int)((long long)P.kb * piece / P.pieces);
+  };
+  auto k_hi = [&](const ProductK& P, int piece) {
+    return S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : (int)((long long)P.kb * (piece + 1) / P.pieces);
+  };
 
   if (warp == 0) {
     if (TMA && elect_one()) {
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const bool gated = P.gated, amn = P.a_mn, bmn = P.b_mn;
         const int n0 = gated ? tl.n * (P.bn / 2) : tl.n * P.bn + (CG == 2 ? (int)rank * brows : 0);
         const int bbytes = brows * BK * 2, subs = g.subs;
-        const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0;
+        const int lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece), kb0 = P.kb0;
         for (int q = 0; q < 2 && ok; ++q) {  // operand pairs
           const CUtensorMap* ma = &P.ma[q];
           const CUtensorMap* mb = gated && CG == 2 ? &P.mb[rank] : &P.mb[q];
@@ -557,7 +570,8 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int t = unit; t < g.tiles && ok; t += units) {  // lt: buffers filled
-        const ProductK& P = g.p[tile_at(g, t).p];
+        const Tile tl = tile_at(g, t);
+        const ProductK& P = g.p[tl.p];
         if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) break;
         tc_fence_after();
         const bool amn = P.a_mn, bmn = P.b_mn;
@@ -567,7 +581,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const uint64_t da0 = smem_desc(0, amn, subs), db0 = smem_desc(0, bmn, subs);
         // bytes from one k-block of a stage to the next
         const uint32_t a_sub = amn ? 8192 : kABytes, b_sub = bmn ? 8192 : bn / CG * BK * 2;
-        const int lo = k_lo(P), hi = k_hi(P), kb0 = P.kb0, seg = seg_blocks(hi - lo);
+        const int lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece), kb0 = P.kb0, seg = seg_blocks(hi - lo);
         uint32_t d = tmem + buf * buf_cols;
         int in = 0;  // k-blocks in the present segment
         for (int kb = lo; kb < hi;) {
@@ -661,18 +675,19 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       const ProductK& P = g.p[tl.p];
       if constexpr (F32) {  // these warps bring the operands in first
         if (P.bn == 128)
-          feed_f32<128>(P, tl.m * BM, tl.n * (P.gated ? 64 : 128), k_lo(P), k_hi(P), te, smem, sbytes, stages, full, empty, feed,
+          feed_f32<128>(P, tl.m * BM, tl.n * (P.gated ? 64 : 128), k_lo(P, tl.piece), k_hi(P, tl.piece), te, smem, sbytes, stages, full, empty, feed,
                         status, abort_flag);
         else
-          feed_f32<64>(P, tl.m * BM, tl.n * (P.gated ? 32 : 64), k_lo(P), k_hi(P), te, smem, sbytes, stages, full, empty, feed,
+          feed_f32<64>(P, tl.m * BM, tl.n * (P.gated ? 32 : 64), k_lo(P, tl.piece), k_hi(P, tl.piece), te, smem, sbytes, stages, full, empty, feed,
                        status, abort_flag);
       }
-      const OpEpi e = P.e;
+      OpEpi e = P.e;
+      if (tl.piece) e.out = reinterpret_cast<float*>(e.out) + (size_t)tl.piece * P.M * e.ld;
       const int bn = P.bn, pM = P.M, pN = P.N;
       const bool gated = P.gated;
       const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
       const int n0 = tl.n * (gated ? bn / 2 : bn);
-      const int n_kb = k_hi(P) - k_lo(P), sg = seg_blocks(n_kb), segs = (n_kb + sg - 1) / sg;
+      const int n_kb = k_hi(P, tl.piece) - k_lo(P, tl.piece), sg = seg_blocks(n_kb), segs = (n_kb + sg - 1) / sg;
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       const int mw = m0 + quad * 32;
       auto ready = [&] {  // the present buffer is complete (one decision for all warps)
@@ -819,8 +834,8 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       const Tile tl = tile_at(g, t);
       const ProductK& P = g.p[tl.p];
       const int m0 = tl.m * BM, n0 = tl.n * (P.gated ? P.bn / 2 : P.bn);
-      const int hi = k_hi(P);
-      for (int kb = k_lo(P); kb < hi; ++kb, ++it) {
+      const int hi = k_hi(P, tl.piece);
+      for (int kb = k_lo(P, tl.piece); kb < hi; ++kb, ++it) {
         // (one answer for the whole warp)
         if (it >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], phase ^ 1, status,
                                                                kStatusTimeoutTmaEmpty, abort_flag))) {
@@ -902,8 +917,9 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
     if (lane == 0) {  // the last commits have arrived before the tensor memory is freed
       int n = 0;
       for (int t = unit; t < g.tiles; t += units) {
-        const ProductK& P = g.p[tile_at(g, t).p];
-        const int n_kb = k_hi(P) - k_lo(P), sg = seg_blocks(n_kb);
+        const Tile tl = tile_at(g, t);
+        const ProductK& P = g.p[tl.p];
+        const int n_kb = k_hi(P, tl.piece) - k_lo(P, tl.piece), sg = seg_blocks(n_kb);
         n += F32 ? 1 : (n_kb + sg - 1) / sg;
       }
       for (int l = max(0, n - nbuf); l < n; ++l)
@@ -984,7 +1000,9 @@ int tile_cols(const OpProduct& p, const Plan& pl) {
   const int n = p.gated ? 2 * ceil_div(p.N, 32) * 32 : p.N;
   return std::min(pl.bn, ceil_div(n, q) * q);
 }
-int k_blocks(const OpProduct& p) { return std::max(1, p.pairs) * ceil_div(p.K, BK); }
+int pieces_of(const OpProduct& p) { return std::max(1, p.pieces); }
+// k-blocks of one of its tiles (the longest piece's)
+int k_blocks(const OpProduct& p) { return ceil_div(std::max(1, p.pairs) * ceil_div(p.K, BK), pieces_of(p)); }
 
 // Estimated ns of a plan, from measured parts: one k-block of a tile (all SMs
 // busy, operands from L2), what follows a tile's last MMA, and the launch.
@@ -1009,7 +1027,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   const double extra = bare ? tail : 150;
   if (n == 1) {
     const int bn = tile_cols(p[0], pl), cols = p[0].gated ? 2 * p[0].N : p[0].N;
-    const long long tiles = (long long)ceil_div(p[0].M, BM * pl.cg) * ceil_div(cols, bn);
+    const long long tiles = (long long)ceil_div(p[0].M, BM * pl.cg) * ceil_div(cols, bn) * pieces_of(p[0]);
     return (double)((tiles + units - 1) / units) * (k_blocks(p[0]) * per(p[0]) + extra) + tail;
   }
   // several products: the busiest unit's tiles
@@ -1019,7 +1037,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   double c[kOpProducts];
   for (int i = 0; i < n; ++i) {
     const long long tiles = (long long)ceil_div(p[i].M, BM * pl.cg) *
-                            ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl));
+                            ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl)) * pieces_of(p[i]);
     c[i] = k_blocks(p[i]) * per(p[i]) + extra;
     first[i] = (int)(pos % units);
     whole[i] = tiles / units;
@@ -1063,7 +1081,7 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
   for (int bn = mode == kF32 ? 128 : 256; bn >= 64; bn -= 32) {  // (fp32: six parts of a wider tile leave no second stage)
     if ((bn & (bn - 1)) && (!narrow || mode == kF32)) continue;
     consider(Plan{1, bn, 1, 1});
-    if (n > 1) continue;
+    if (n > 1 || pieces_of(p[0]) > 1) continue;
     const int cols = tile_cols(p[0], Plan{1, bn, 1, 1});
     const long long tiles = (long long)ceil_div(p[0].M, BM) * ceil_div(p[0].gated ? 2 * p[0].N : p[0].N, cols);
     for (int s = 2; s <= 8; ++s)
@@ -1117,13 +1135,14 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
     ProductK& k = g.p[i];
     k.M = q.M;
     k.N = q.N;
-    k.kb = k_blocks(q);
+    k.kb = std::max(1, q.pairs) * ceil_div(q.K, BK);
     k.kb0 = ceil_div(q.K, BK);
     k.bn = tile_cols(q, pl);
     k.tiles_m = ceil_div(q.M, BM * pl.cg);
     k.tiles_n = ceil_div(q.N, q.gated ? k.bn / 2 : k.bn);
     k.tile0 = tiles;
-    tiles += k.tiles_m * k.tiles_n;
+    k.pieces = std::max(1, q.pieces);
+    tiles += k.tiles_m * k.tiles_n * k.pieces;
     k.a_mn = q.a_mn;
     k.b_mn = q.b_mn;
     k.gated = q.gated;

@@ -435,7 +435,15 @@ struct OpProduct {
   int pairs;  // 1 or 2 (2: gated is 0)
   int M, N, K;
   int a_mn, b_mn, gated;
+  int pieces;  // > 1: the reduction in so many shares, e.out = fp32 [pieces][M][ld] (0: 1)
   OpEpi e;
+};
+// Sums of a product's pieces, out[i] = sum_p part[p][i], in the type asked for.
+struct OpPartSum {
+  const float* part;
+  void* out;
+  size_t n;
+  int pieces, f32;
 };
 
 // Column sums of partial rows, out[c] = sum_r part[r][c], added by the
@@ -464,6 +472,7 @@ struct ActGrad {
   int M, N, ld_dz, act, f32, dy_f32, chunks;
 };
 int act_grad_chunks(int M, int N, bool f32);
+cudaError_t launch_part_sums(const OpPartSum* sums, int n, cudaStream_t s);
 // The sums alone (a call that wants no product).
 cudaError_t launch_col_sum(const OpColSum* sums, int n, cudaStream_t s);
 cudaError_t launch_act_grad(const ActGrad& a, cudaStream_t s);

@@ -62,13 +62,43 @@ cudaError_t products(int dtype, const OpProduct* p, int n, const OpColSum* sums,
   return launch_op_gemm(p, n, dtype == WAM_FP32, sums, n_sums, s);
 }
 
+// Shares of the two gradients' reductions.  A gradient with few tiles and a
+// long reduction (the weights' of a narrow layer over many rows, the input's
+// of few rows through a wide one) would keep a few SMs busy after the rest are
+// done: its reduction is cut so that no tile takes longer than an SM's part
+// of all the work, at least `least` k-blocks each, and the pieces (fp32, in the
+// workspace) are added by a kernel after it.  linear 5128 rows, 271 x 74 fp32:
+// 149 us whole, 36 us in pieces.
+struct Pieces {
+  int dx, dw;
+};
+Pieces pieces_for(int dtype, int M, int N, int K, int sides) {
+  constexpr int kSms = 148;
+  const int bn = dtype == WAM_FP32 ? 64 : 128, least = dtype == WAM_FP32 ? 4 : 12;
+  const double over = dtype == WAM_FP32 ? 5 : 6;  // a tile's fixed part, in k-blocks
+  const double cols = (K + bn - 1) / bn;
+  const double tx = (M + 127) / 128 * cols, tw = sides * ((N + 127) / 128 * cols);
+  const int kx = sides * ((N + 63) / 64), kw = (M + 63) / 64;
+  const double share = (tx * (kx + over) + tw * (kw + over)) / kSms;
+  auto cut = [&](int kb, double elements) {
+    const double t = share > least ? share : least;
+    if (kb < 1.5 * t) return 1;
+    int p = (int)(kb / t + 0.999);
+    if (p > 16) p = 16;
+    while (p > 1 && p * elements * 4 > 32e6) --p;  // (the pieces stay in L2)
+    return p;
+  };
+  return {cut(kx, (double)M * K), cut(kw, (double)sides * N * K)};
+}
 // Workspace of a backward pass, in order: the activation's gradients (one or
 // two [M, N8] matrices of the compute type), the bias gradients' partial sums,
-// and, on the bf16 path when K is not a multiple of 8, copies of x and of the
-// weights with padded rows (the tensor-core loads start on 16 bytes).
+// on the bf16 path when K is not a multiple of 8 copies of x and of the
+// weights with padded rows (the tensor-core loads start on 16 bytes), and the
+// pieces of the gradients' reductions.
 struct BwdLayout {
-  size_t dz, part, x, w, total;
+  size_t dz, part, x, w, px, pw, total;
   int ldn, ldk;
+  Pieces cut;
 };
 BwdLayout bwd_layout(int dtype, int M, int N, int K, int sides, bool need_dz) {
   BwdLayout l{};
@@ -83,9 +113,26 @@ BwdLayout bwd_layout(int dtype, int M, int N, int K, int sides, bool need_dz) {
   if (dtype == WAM_BF16 && K % 8) at += up((size_t)M * l.ldk * 2);
   l.w = at;
   if (dtype == WAM_BF16 && K % 8) at += sides * up((size_t)N * l.ldk * 2);
+  l.cut = pieces_for(dtype, M, N, K, sides);
+  l.px = at;
+  if (l.cut.dx > 1) at += up((size_t)l.cut.dx * M * K * 4);
+  l.pw = at;
+  if (l.cut.dw > 1) at += sides * up((size_t)l.cut.dw * N * K * 4);
   l.total = at;
   return l;
 }
+// A gradient's epilogue: the output itself, or its pieces and the sum of them.
+void gradient_out(OpProduct& q, void* out, int pieces, char* part, bool f32, OpPartSum* sums, int* n_sums) {
+  q.pieces = pieces;
+  if (pieces > 1) {
+    q.e = epilogue(part, q.N, true);
+    sums[(*n_sums)++] = {reinterpret_cast<const float*>(part), out, (size_t)q.M * q.N, pieces, f32};
+  } else {
+    q.e = epilogue(out, q.N, f32);
+  }
+  set_vec(q.e);
+}
+
 // The incoming gradient is the product's operand as it stands.
 bool direct(int dtype, int N, int act, int dy_dtype) {
   return act == kActNone && dy_dtype == dtype && (dtype == WAM_FP32 || N % 8 == 0);
@@ -193,7 +240,8 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
   }
   const OpMat dz = as_is ? OpMat{dy, N, N, M} : OpMat{ws + l.dz, l.ldn, N, M};
   OpProduct p[2] = {};
-  int n = 0;
+  OpPartSum ps[2];
+  int n = 0, n_ps = 0;
   auto add_dx = [&] {  // dx = dz W
     OpProduct& q = p[n++];
     q.a[0] = dz;
@@ -203,8 +251,7 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
     q.N = K;
     q.K = N;
     q.b_mn = 1;
-    q.e = epilogue(dx, K, dtype == WAM_FP32);
-    set_vec(q.e);
+    gradient_out(q, dx, l.cut.dx, ws + l.px, dtype == WAM_FP32, ps, &n_ps);
   };
   auto add_dw = [&] {  // dW = dz^T x
     OpProduct& q = p[n++];
@@ -215,16 +262,18 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
     q.N = K;
     q.K = M;
     q.a_mn = q.b_mn = 1;
-    q.e = epilogue(dw, K, dtype == WAM_FP32);
-    set_vec(q.e);
+    gradient_out(q, dw, l.cut.dw, ws + l.pw, dtype == WAM_FP32, ps, &n_ps);
   };
-  // the longer reduction first: the last wave is made of the shorter tiles
-  if (dx && N >= M) add_dx();
+  // the longer tiles first: the last wave is made of the shorter ones
+  const bool dx_first = (double)N / l.cut.dx >= (double)M / l.cut.dw;
+  if (dx && dx_first) add_dx();
   if (dw) add_dw();
-  if (dx && N < M) add_dx();
+  if (dx && !dx_first) add_dx();
   const OpColSum cs{part, db, chunks, N};
   if (n == 0) return status_of(launch_col_sum(&cs, 1, s));
-  return status_of(products(dtype, p, n, &cs, db ? 1 : 0, s));
+  err = products(dtype, p, n, &cs, db ? 1 : 0, s);
+  if (err == cudaSuccess && n_ps) err = launch_part_sums(ps, n_ps, s);
+  return status_of(err);
 }
 
 // ------------------------------------------------------------------- gated --
@@ -328,7 +377,8 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
     wu = u8;
   }
   OpProduct p[3] = {};
-  int n = 0;
+  OpPartSum ps[3];
+  int n = 0, n_ps = 0;
   auto add_dx = [&] {  // dx = dg Wg + du Wu
     OpProduct& q = p[n++];
     q.a[0] = {dg, l.ldn, F, M};
@@ -340,10 +390,10 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
     q.N = K;
     q.K = F;
     q.b_mn = 1;
-    q.e = epilogue(dx, K, dtype == WAM_FP32);
-    set_vec(q.e);
+    gradient_out(q, dx, l.cut.dx, ws + l.px, dtype == WAM_FP32, ps, &n_ps);
   };
-  auto add_dw = [&](const void* d, void* out) {
+  const size_t piece_w = up((size_t)l.cut.dw * F * K * 4);
+  auto add_dw = [&](const void* d, void* out, int side) {
     OpProduct& q = p[n++];
     q.a[0] = {d, l.ldn, F, M};
     q.b[0] = {x, ldk, K, M};
@@ -352,19 +402,20 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
     q.N = K;
     q.K = M;
     q.a_mn = q.b_mn = 1;
-    q.e = epilogue(out, K, dtype == WAM_FP32);
-    set_vec(q.e);
+    gradient_out(q, out, l.cut.dw, ws + l.pw + side * piece_w, dtype == WAM_FP32, ps, &n_ps);
   };
-  const bool dx_first = 2ll * F >= M;
+  const bool dx_first = 2.0 * F / l.cut.dx >= (double)M / l.cut.dw;
   if (dx && dx_first) add_dx();
   if (dwg) {
-    add_dw(dg, dwg);
-    add_dw(du, dwu);
+    add_dw(dg, dwg, 0);
+    add_dw(du, dwu, 1);
   }
   if (dx && !dx_first) add_dx();
   const OpColSum cs[2] = {{part, dbias_g, chunks, F}, {part ? part + (size_t)chunks * F : nullptr, dbias_u, chunks, F}};
   if (n == 0) return status_of(launch_col_sum(cs, 2, s));
-  return status_of(products(dtype, p, n, cs, dbias_g ? 2 : 0, s));
+  err = products(dtype, p, n, cs, dbias_g ? 2 : 0, s);
+  if (err == cudaSuccess && n_ps) err = launch_part_sums(ps, n_ps, s);
+  return status_of(err);
 }
 
 // ----------------------------------------------------------- residual norm --

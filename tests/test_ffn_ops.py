@@ -122,7 +122,9 @@ def test_workspace_sizes():
     assert W.op_linear_act_workspace(W.BF16, 1000, 512, 256, act=2) >= small + 1000 * 512 * 2
     assert W.op_linear_act_workspace(W.BF16, 1000, 513, 256) >= 1000 * 520 * 2  # rows padded to 16 bytes
     assert W.op_linear_act_workspace(W.BF16, 1000, 512, 257) >= (1000 + 512) * 264 * 2  # operands copied
-    assert W.op_linear_act_workspace(W.FP32, 1000, 513, 257, act=1) < 1000 * 520 * 4 + (1 << 20)
+    assert W.op_linear_act_workspace(W.FP32, 1000, 513, 257, act=1) < 1000 * 520 * 4 + 16 * 513 * 257 * 4
+    # a narrow layer over many rows: its weight gradient's reduction in pieces
+    assert W.op_linear_act_workspace(W.BF16, 8192, 128, 128) >= 2 * 128 * 128 * 4
     assert W.op_gated_workspace(W.BF16, 100, 200, 64) >= 2 * 100 * 200 * 2
     assert W.op_residual_norm_workspace(0, 64) == 0
     assert W.op_residual_norm_workspace(100, 64, 1) == 100 * 3 * 64 * 4

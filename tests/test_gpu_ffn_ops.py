@@ -347,6 +347,27 @@ def test_linear_forms(M, N, K, o, res):
         assert ((y.double() - y64).norm() / y64.norm()).item() < 1e-6
 
 
+@pytest.mark.parametrize("M,N,K,t", [(9000, 100, 72, BF), (9000, 70, 130, BF), (40, 5000, 200, BF), (5128, 271, 74, FP), (43, 3000, 520, FP)])
+def test_gradients_in_pieces(M, N, K, t):
+    """Few tiles and a long reduction: it is cut into pieces that are added afterwards."""
+    n = T.normals(M + N)
+    x, w, dy, z = n(M, K, dtype=t), n(N, K, std=K ** -0.5, dtype=t), n(M, N, dtype=t), n(M, N, dtype=t)
+    (dx, ok1), (dw, ok2), db = T.guarded((M, K), t), T.guarded((N, K), t), torch.empty(N, device="cuda")
+    ws = _ws(W.op_linear_act_workspace(CODE[t], M, N, K, act=ACT["silu"]))
+    W.op_linear_act_backward(CODE[t], x, w, z, dy, dx, dw, db, M, N, K, act=ACT["silu"], workspace=ws)
+    (dx64, ex), [((dw64, ew), (db64, eb))] = T.linear_grad64(x, w, z, dy, "silu")
+    T.within(dx, dx64, ex), T.within(dw, dw64, ew), T.within(db, db64, eb)
+    ok1(), ok2()
+    a, b = torch.empty_like(dx), torch.empty_like(dw)
+    W.op_linear_act_backward(CODE[t], x, w, z, dy, a, b, db, M, N, K, act=ACT["silu"], workspace=ws)
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+    wu, u = n(N, K, std=K ** -0.5, dtype=t), n(M, N, dtype=t)
+    outs = [torch.empty_like(dx), torch.empty_like(dw), torch.empty_like(dw)]
+    W.op_gated_backward(CODE[t], x, w, wu, z, u, dy, *outs, M, N, K, workspace=_ws(W.op_gated_workspace(CODE[t], M, N, K)))
+    (dx64, ex), [((g64, eg), _), ((u64, eu), _)] = T.gated_grad64(x, w, wu, z, u, dy, "silu")
+    T.within(outs[0], dx64, ex), T.within(outs[1], g64, eg), T.within(outs[2], u64, eu)
+
+
 def test_fp32_products_are_fp32():
     """Three parts an operand: the sums are as near as an fp32 matrix product's, at any scale of the operands."""
     M, N, K = 200, 300, 1500
