@@ -88,6 +88,13 @@ __global__ void __launch_bounds__(32 * kRows, kBlocksPerSm) act_grad_kernel(cons
       }
     }
   }
+  // fp32 rows that end inside a vector: the rest of it is zero (the product
+  // takes it as part of the row)
+  if (E == 1 && F32 && a.dz && n >= a.N && n < (a.N + 3) / 4 * 4)
+    for (int r = lo + ty; r < hi; r += kRows) {
+      reinterpret_cast<float*>(a.dz)[(size_t)r * a.ld_dz + n] = 0.f;
+      if (GATED) reinterpret_cast<float*>(a.du)[(size_t)r * a.ld_dz + n] = 0.f;
+    }
   if (!a.part) return;
 #pragma unroll
   for (int j = 0; j < E; ++j) {
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(32 * kRows, kBlocksPerSm) act_grad_kernel(cons
 
 template <int E, bool GATED, typename T, typename DY, bool ANY = false>
 cudaError_t run(const ActGrad& a, cudaStream_t s) {
-  const dim3 grid((a.N + 32 * E - 1) / (32 * E), a.chunks);
+  const dim3 grid(((a.dz && E == 1 ? (a.N + 3) / 4 * 4 : a.N) + 32 * E - 1) / (32 * E), a.chunks);
   return launch_k(act_grad_kernel<E, GATED, T, DY, ANY>, grid, dim3(32, kRows), 0, s, a);
 }
 template <int E, typename T>

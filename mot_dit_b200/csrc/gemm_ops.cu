@@ -334,26 +334,38 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   mid = pack_bf16(a, b);
   lo = pack_bf16(a - bf16_lo(mid), b - bf16_hi(mid));
 }
-// Eight elements [col, col + 8) of a row, zero outside the matrix.
+// Eight elements [col, col + 8) of a row, zero outside the matrix.  VEC: rows
+// start on 16 bytes and hold whole vectors (nothing here may touch what is loaded:
+// it would wait for the load).
+template <bool VEC>
 __device__ __forceinline__ void fetch8_f32(const OpMat& m, int row, int col, float4& x, float4& y) {
   x = y = make_float4(0.f, 0.f, 0.f, 0.f);
   if (row >= m.outer || col >= m.inner) return;
   const float* p = reinterpret_cast<const float*>(m.p) + (size_t)row * m.ld + col;
-  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && col + 8 <= m.inner) {
+  if constexpr (VEC) {
+    const int n = m.inner - col;
     x = reinterpret_cast<const float4*>(p)[0];
-    y = reinterpret_cast<const float4*>(p)[1];
-    return;
+    if (n > 4) y = reinterpret_cast<const float4*>(p)[1];
+  } else {
+    const int n = m.inner - col;
+    x.x = p[0];
+    if (n > 1) x.y = p[1];
+    if (n > 2) x.z = p[2];
+    if (n > 3) x.w = p[3];
+    if (n > 4) y.x = p[4];
+    if (n > 5) y.y = p[5];
+    if (n > 6) y.z = p[6];
+    if (n > 7) y.w = p[7];
   }
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = col + j < m.inner ? p[j] : 0.f;
-  x = make_float4(v[0], v[1], v[2], v[3]);
-  y = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ bool vec_f32(const OpMat& m) {
+  return ((reinterpret_cast<uintptr_t>(m.p) & 15) | (m.ld & 3) | (m.inner & 3)) == 0;
 }
 // k-blocks [lo, hi) of a 128 x BN tile: 256 threads, 16-byte chunks of the
 // swizzled tiles; the next block's elements are requested as soon as the
-// present ones are on their way to shared memory.
-template <int BN>
+// present ones are on their way to shared memory.  (VA, VB: fetch8_f32's VEC of either operand;
+// parameters, so that the loop holds one kind of load: its instructions have to stay in the cache.)
+template <int BN, bool VA, bool VB>
 __device__ __forceinline__ void feed_f32(const ProductK& P, int m0, int n0, int lo, int hi, int te, uint8_t* smem, int sbytes,
                                          int stages, uint64_t* full, uint64_t* empty, Feed& f, unsigned* status,
                                          volatile int* abort) {
@@ -368,19 +380,19 @@ __device__ __forceinline__ void feed_f32(const ProductK& P, int m0, int n0, int 
     for (int i = 0; i < NA; ++i) {
       const int c = te + i * 256, r = c >> 3, k = (c & 7) * 8;
       if (amn)
-        fetch8_f32(A, kk + (r & 63), m0 + (r >> 6) * 64 + k, v[i][0], v[i][1]);
+        fetch8_f32<VA>(A, kk + (r & 63), m0 + (r >> 6) * 64 + k, v[i][0], v[i][1]);
       else
-        fetch8_f32(A, m0 + r, kk + k, v[i][0], v[i][1]);
+        fetch8_f32<VA>(A, m0 + r, kk + k, v[i][0], v[i][1]);
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int c = te + i * 256, r = c >> 3, k = (c & 7) * 8;
       if (bmn)
-        fetch8_f32(B0, kk + (r & 63), n0 + (r >> 6) * 64 + k, v[NA + i][0], v[NA + i][1]);
+        fetch8_f32<VB>(B0, kk + (r & 63), n0 + (r >> 6) * 64 + k, v[NA + i][0], v[NA + i][1]);
       else if (gated)
-        fetch8_f32(r < BN / 2 ? B0 : B1, n0 + r % (BN / 2), kk + k, v[NA + i][0], v[NA + i][1]);
+        fetch8_f32<VB>(r < BN / 2 ? B0 : B1, n0 + r % (BN / 2), kk + k, v[NA + i][0], v[NA + i][1]);
       else
-        fetch8_f32(B0, n0 + r, kk + k, v[NA + i][0], v[NA + i][1]);
+        fetch8_f32<VB>(B0, n0 + r, kk + k, v[NA + i][0], v[NA + i][1]);
     }
   };
   load(lo);
@@ -674,12 +686,22 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       const Tile tl = tile_at(g, t);
       const ProductK& P = g.p[tl.p];
       if constexpr (F32) {  // these warps bring the operands in first
-        if (P.bn == 128)
-          feed_f32<128>(P, tl.m * BM, tl.n * (P.gated ? 64 : 128), k_lo(P, tl.piece), k_hi(P, tl.piece), te, smem, sbytes, stages, full, empty, feed,
-                        status, abort_flag);
-        else
-          feed_f32<64>(P, tl.m * BM, tl.n * (P.gated ? 32 : 64), k_lo(P, tl.piece), k_hi(P, tl.piece), te, smem, sbytes, stages, full, empty, feed,
-                       status, abort_flag);
+        const bool va = vec_f32(P.a[0]) && vec_f32(P.a[1]), vb = vec_f32(P.b[0]) && vec_f32(P.b[1]);
+        const int m0_ = tl.m * BM, n0_ = tl.n * (P.gated ? P.bn / 2 : P.bn), lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece);
+#define WAM_FEED(BN, VA, VB) \
+  feed_f32<BN, VA, VB>(P, m0_, n0_, lo, hi, te, smem, sbytes, stages, full, empty, feed, status, abort_flag)
+        if (P.bn == 128) {
+          if (va)
+            vb ? WAM_FEED(128, true, true) : WAM_FEED(128, true, false);
+          else
+            vb ? WAM_FEED(128, false, true) : WAM_FEED(128, false, false);
+        } else {
+          if (va)
+            vb ? WAM_FEED(64, true, true) : WAM_FEED(64, true, false);
+          else
+            vb ? WAM_FEED(64, false, true) : WAM_FEED(64, false, false);
+        }
+#undef WAM_FEED
       }
       OpEpi e = P.e;
       if (tl.piece) e.out = reinterpret_cast<float*>(e.out) + (size_t)tl.piece * P.M * e.ld;

@@ -238,7 +238,8 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
     if ((err = launch_repack(w, ws + l.w, N, K, ldk, s)) != cudaSuccess) return status_of(err);
     w = ws + l.w;
   }
-  const OpMat dz = as_is ? OpMat{dy, N, N, M} : OpMat{ws + l.dz, l.ldn, N, M};
+  const int in = dtype == WAM_FP32 ? (N + 3) / 4 * 4 : N;  // (fp32: whole vectors, zero past N)
+  const OpMat dz = as_is ? OpMat{dy, N, N, M} : OpMat{ws + l.dz, l.ldn, in, M};
   OpProduct p[2] = {};
   OpPartSum ps[2];
   int n = 0, n_ps = 0;
@@ -376,13 +377,14 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
     wg = g8;
     wu = u8;
   }
+  const int in = dtype == WAM_FP32 ? (F + 3) / 4 * 4 : F;  // (fp32: whole vectors, zero past F)
   OpProduct p[3] = {};
   OpPartSum ps[3];
   int n = 0, n_ps = 0;
   auto add_dx = [&] {  // dx = dg Wg + du Wu
     OpProduct& q = p[n++];
-    q.a[0] = {dg, l.ldn, F, M};
-    q.a[1] = {du, l.ldn, F, M};
+    q.a[0] = {dg, l.ldn, in, M};
+    q.a[1] = {du, l.ldn, in, M};
     q.b[0] = {wg, ldk, K, F};
     q.b[1] = {wu, ldk, K, F};
     q.pairs = 2;
@@ -395,7 +397,7 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
   const size_t piece_w = up((size_t)l.cut.dw * F * K * 4);
   auto add_dw = [&](const void* d, void* out, int side) {
     OpProduct& q = p[n++];
-    q.a[0] = {d, l.ldn, F, M};
+    q.a[0] = {d, l.ldn, in, M};
     q.b[0] = {x, ldk, K, M};
     q.pairs = 1;
     q.M = F;
