@@ -391,10 +391,13 @@ wam_status wam_op_attention_noalloc(const void* dev_q, const void* dev_k, const 
 /* ---- feed-forward and residual-norm operators, both directions --------- */
 
 /* What the entry points below share.
- *   - Types: dtype WAM_BF16 (bf16 matrices, products on the tensor cores, fp32
- *     accumulation) or WAM_FP32 (fp32 everywhere).  Every sum, statistic and
- *     activation is fp32; an output is rounded once.  Biases, gains,
- *     modulation vectors and their gradients are fp32.
+ *   - Types: dtype WAM_BF16 (bf16 matrices) or WAM_FP32 (fp32 matrices).  Every
+ *     sum, statistic and activation is fp32; an output is rounded once.
+ *     Biases, gains, modulation vectors and their gradients are fp32.  fp32
+ *     products run on the tensor cores, each operand as the exact sum of three
+ *     bf16 parts (the result is as near to the exact one as an fp32 sum's;
+ *     magnitudes above 3.38e38 count as infinite, and an infinite operand
+ *     gives NaN where it meets a value with a zero part).
  *   - Matrices are row-major and contiguous, aligned to their element; any
  *     M >= 0 and any sizes from 1 up.  16-byte-aligned pointers and row
  *     lengths that are multiples of 8 are fastest.  M == 0: outputs with rows

@@ -34,6 +34,7 @@
 // loaders.  No load is multicast.  Every wait is bounded (op_gemm_status).
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "cluster.cuh"
 #include "kernels.h"
@@ -962,6 +963,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
 // ------------------------------------------------------------------- host --
 struct Device {
   std::atomic<int> ready{0};
+  std::mutex fill;
   int sms = 148;
   int clusters[9];  // clusters of n CTAs (one per SM) that run at once
 };
@@ -973,7 +975,9 @@ cudaError_t device_info(Device** out) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   Device& d = g_dev[dev];
-  if (!d.ready.load(std::memory_order_acquire)) {  // (idempotent: two threads may both do it)
+  std::unique_lock<std::mutex> lock(d.fill, std::defer_lock);
+  if (!d.ready.load(std::memory_order_acquire)) lock.lock();
+  if (lock.owns_lock() && !d.ready.load(std::memory_order_relaxed)) {
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(op_gemm_kernel<1, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess ||

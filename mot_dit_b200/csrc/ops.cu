@@ -13,6 +13,7 @@ constexpr int kMaxDim = 1 << 24;  // rows, features (tile and chunk counts stay 
 
 wam_status status_of(cudaError_t e) {
   if (e == cudaSuccess) return WAM_OK;
+  (void)cudaGetLastError();  // a refused launch is reported here, not by the caller's next call
   if (e == cudaErrorMemoryAllocation) return WAM_ERR_OOM;
   return WAM_ERR_CUDA;
 }

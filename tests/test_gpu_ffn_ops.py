@@ -368,6 +368,80 @@ def test_gradients_in_pieces(M, N, K, t):
     T.within(outs[0], dx64, ex), T.within(outs[1], g64, eg), T.within(outs[2], u64, eu)
 
 
+@pytest.mark.parametrize("t", [BF, FP])
+def test_backward_unaligned(t):
+    """Every operand of the backward passes off a 16-byte boundary, one by one and together."""
+    M, N, K = 150, 136, 200
+    put = lambda v, s: torch.cat([torch.zeros(s, dtype=v.dtype, device="cuda"), v.flatten()])[s:].view(v.shape)  # noqa: E731
+    for which in ("x", "w", "dy", "z", "out", "all"):
+        n = T.normals(9)
+        off = lambda k: 1 if which in (k, "all") else 0  # noqa: E731
+        x, w = put(n(M, K, dtype=t), off("x")), put(n(N, K, std=K ** -0.5, dtype=t), off("w"))
+        dy, z, u = put(n(M, N, dtype=t), off("dy")), put(n(M, N, dtype=t), off("z")), put(n(M, N, dtype=t), off("z"))
+        (dx, ok1), (dw, ok2), (du, ok3) = (T.guarded(s, t, off("out")) for s in ((M, K), (N, K), (N, K)))
+        db = torch.empty(N, device="cuda")
+        for act, pre in (("none", None), ("gelu_tanh", z)):
+            W.op_linear_act_backward(CODE[t], x, w, pre, dy, dx, dw, db, M, N, K, act=ACT[act],
+                                     workspace=_ws(W.op_linear_act_workspace(CODE[t], M, N, K, act=ACT[act])))
+            (dx64, ex), [((dw64, ew), (db64, eb))] = T.linear_grad64(x, w, pre, dy, act)
+            T.within(dx, dx64, ex), T.within(dw, dw64, ew), T.within(db, db64, eb)
+        W.op_gated_backward(CODE[t], x, w, w, z, u, dy, dx, dw, du, M, N, K, workspace=_ws(W.op_gated_workspace(CODE[t], M, N, K)))
+        (dx64, ex), [((g64, eg), _), ((u64, eu), _)] = T.gated_grad64(x, w, w, z, u, dy, "silu")
+        T.within(dx, dx64, ex), T.within(dw, g64, eg), T.within(du, u64, eu)
+        ok1(), ok2(), ok3()
+
+
+@pytest.mark.parametrize("D", [7, 64, 1000, 4100, 8000])
+@pytest.mark.parametrize("t", [BF, FP])
+def test_residual_norm_unaligned(D, t):
+    """Streams and outputs off a 16-byte boundary give the bits that a row's own arithmetic gives elsewhere."""
+    M = 9
+    n = T.normals(D)
+    put = lambda v, s: torch.cat([torch.zeros(s, dtype=v.dtype, device="cuda"), v.flatten()])[s:].view(v.shape)  # noqa: E731
+    x, y, g, ds, dh = n(M, D, dtype=t), n(M, D, dtype=t), n(D), n(M, D, dtype=t), n(M, D, dtype=t)
+    kw = dict(post_norm=True, gain=g, res_dtype=CODE[t])
+    want, got = [], []
+    for s, out in ((0, want), (1, got)):
+        (sv, ok1), (h, ok2), (dx, ok3), (dy, ok4) = (T.guarded((M, D), t, s) for _ in range(4))
+        W.op_residual_norm(CODE[t], put(x, s), put(y, s), sv, h, M, D, **kw)
+        W.op_residual_norm_backward(CODE[t], put(x, s), put(y, s), put(ds, s), put(dh, s), dx, dy, M, D, **kw)
+        ok1(), ok2(), ok3(), ok4()
+        out += [sv, h, dx, dy]
+    for a, b in zip(want, got):  # (the order of a row's sums differs: a step or two)
+        assert torch.isfinite(b).all()
+        assert (a.double() - b.double()).norm() <= 2 * T.H[t] * a.double().norm() + 1e-5 * a.double().norm()
+
+
+def test_first_call_in_a_capture():
+    """A process whose first call of the operators is a captured one."""
+    import subprocess
+    import sys
+    code = """
+import torch, sys
+import mot_dit_b200 as W
+torch.cuda.init()
+n = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+x, w, y, a, h = n(200, 256), n(512, 256), n(200, 512), n(200, 512), n(200, 256)
+s = torch.randn(200, 256, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    st = torch.cuda.current_stream()
+    W.op_gated(W.BF16, x, w, w, a, 200, 512, 256, stream=st)
+    W.op_linear_act(W.BF16, x, w, None, y, 200, 512, 256, act=2, stream=st)
+    W.op_residual_norm(W.BF16, s, x, s, h, 200, 256, post_norm=True, stream=st)
+g.replay()
+torch.cuda.synchronize()
+z = x.double() @ w.double().t()
+want = torch.nn.functional.silu(z)
+assert ((y.double() - want).norm() / want.norm()).item() < 2.0 ** -7
+assert ((a.double() - want * z).norm() / (want * z).norm()).item() < 2.0 ** -7
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 def test_fp32_products_are_fp32():
     """Three parts an operand: the sums are as near as an fp32 matrix product's, at any scale of the operands."""
     M, N, K = 200, 300, 1500
