@@ -162,6 +162,33 @@ struct Coef {
   }
 };
 
+// Two fp32 operations an instruction (the rows without vector accesses are
+// bound by issue).
+__device__ __forceinline__ unsigned long long bits2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2f(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Barrier of the block's n row threads (the producer warp is not among them).
 __device__ __forceinline__ void row_bar(int n) { asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory"); }
 
@@ -186,9 +213,10 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, i
     for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(all, v[0], o);
     if (lane == 0) b[warp * 8] = v[0];
     row_bar(n);
-    float a = 0.f;
-    for (int i = 0; i < warps; ++i) a += b[i * 8];
-    v[0] = a;
+    float a = lane < warps ? b[lane * 8] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(all, a, o);
+    v[0] = __shfl_sync(all, a, 0);
   } else {
     static_assert(K == 6, "1 or 6 values");
     float x[4], y[2], z;
@@ -205,14 +233,15 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int t, int tpr, int ry, i
     z += __shfl_xor_sync(all, z, 1);
     if ((lane & 3) == 0) b[warp * 8 + (lane >> 2)] = z;  // lane bits 4, 3, 2 = the value's number
     row_bar(n);
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < warps; ++i) {
-      const float4 p = *reinterpret_cast<const float4*>(b + i * 8);
-      const float2 q = *reinterpret_cast<const float2*>(b + i * 8 + 4);
-      s[0] += p.x, s[1] += p.y, s[2] += p.z, s[3] += p.w, s[4] += q.x, s[5] += q.y;
-    }
+    // lane: value lane % 8 of warps lane / 8, + 4, ...
+    float a = 0.f;
 #pragma unroll
-    for (int k = 0; k < 6; ++k) v[k] = s[k];
+    for (int i = 0; i < 4; ++i)
+      if ((lane >> 3) + 4 * i < warps) a += b[((lane >> 3) + 4 * i) * 8 + (lane & 7)];
+    a += __shfl_xor_sync(all, a, 8);
+    a += __shfl_xor_sync(all, a, 16);
+#pragma unroll
+    for (int k = 0; k < 6; ++k) v[k] = __shfl_sync(all, a, k);
   }
 }
 
@@ -439,9 +468,9 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
   uint32_t full_phase = 0;
   Coef<E, NV> cf(smem + ring.stages * ring.stage_bytes, D, t, tpr);
   cf.set(f, grp);
-  float sa[NV], sb[NV], sq[NV];
+  f2 sa[NV / 2], sb[NV / 2], sq[NV / 2];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) sa[j] = sb[j] = sq[j] = 0.f;
+  for (int j = 0; j < NV / 2; ++j) sa[j] = sb[j] = sq[j] = bits2(0.f, 0.f);
   const float inv = 1.f / (float)D;
   for (int m0 = lo; m0 < hi; m0 += R) {
     const int m = m0 + ry;
@@ -454,15 +483,22 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
     const CT* ph = staged<CT>(stage, ring.off[2], a.dh, m0, D, ry);
     const RT* pd = staged<RT>(stage, ring.off[3], a.ds, m0, D, ry);
     const int Dd = a.ds ? Dl : 0;
-    float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float s[8], y[8], dh[8], dv[8], mul[8], w[8];
+    f2 v2[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v2[i] = bits2(0.f, 0.f);
+    f2 s[4], y[4], dh[4], dv[4], mul[4], w[4];
+    auto pack = [](const float(&f)[8], f2(&o)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = bits2(f[2 * j], f[2 * j + 1]);
+    };
     auto get = [&](int k) {
-      row_get<E>(ps, Dl, t, tpr, k, s);
-      row_get<E>(ph, Dl, t, tpr, k, dh);
-      row_get<E>(py, Dl, t, tpr, k, y);
-      row_get<E>(pd, Dd, t, tpr, k, dv);
-      cf.mul(k, mul);
-      cf.w(k, w);
+      float f[8];
+      row_get<E>(ps, Dl, t, tpr, k, f), pack(f, s);
+      row_get<E>(ph, Dl, t, tpr, k, f), pack(f, dh);
+      row_get<E>(py, Dl, t, tpr, k, f), pack(f, y);
+      row_get<E>(pd, Dd, t, tpr, k, f), pack(f, dv);
+      cf.mul(k, f), pack(f, mul);
+      cf.w(k, f), pack(f, w);
     };
     auto done = [&] {
       __syncwarp();
@@ -473,15 +509,22 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
     for (int k = 0; k < NV / 8; ++k) {
       get(k);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dn = dh[j] * mul[j], wy = w[j] * y[j];
-        v[0] += s[j] * s[j];
-        v[1] += dn * s[j];
-        v[2] += y[j] * y[j];
-        v[3] += wy * dv[j];
-        v[4] += wy * dn;
-        v[5] += wy * s[j];
+      for (int j = 0; j < 4; ++j) {
+        const f2 dn = mul2(dh[j], mul[j]), wy = mul2(w[j], y[j]);
+        v2[0] = fma2(s[j], s[j], v2[0]);
+        v2[1] = fma2(dn, s[j], v2[1]);
+        v2[2] = fma2(y[j], y[j], v2[2]);
+        v2[3] = fma2(wy, dv[j], v2[3]);
+        v2[4] = fma2(wy, dn, v2[4]);
+        v2[5] = fma2(wy, s[j], v2[5]);
       }
+    }
+    float v[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      float a0, a1;
+      split2f(v2[i], a0, a1);
+      v[i] = a0 + a1;
     }
     if (KEEP) done();
     row_sum<6>(v, t, tpr, ry, R, sh, phase, n);
@@ -489,32 +532,42 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
     const float c = r * r * r * (v[1] * inv);
     const float rp = f.post ? rsqrtf(v[2] * inv + kEps) : 1.f;
     const float cy = f.post ? rp * rp * inv * (v[3] + r * v[4] - c * v[5]) : 0.f;
+    const f2 r2 = bits2(r, r), nc2 = bits2(-c, -c), rp2 = bits2(rp, rp), ncy2 = bits2(-cy, -cy), al2 = bits2(f.alpha, f.alpha);
 #pragma unroll
     for (int k = 0; k < NV / 8; ++k) {
       if (!KEEP) get(k);
+      float o0[8], o1[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dv[j] = dv[j] + r * dh[j] * mul[j] - s[j] * c;
-        sa[8 * k + j] += dh[j] * s[j] * r;
-        sb[8 * k + j] += dh[j];
-        sq[8 * k + j] += dv[j] * (y[j] * rp);
-        y[j] = rp * (dv[j] * w[j] - y[j] * cy);  // (rp = 1, cy = 0 without the norm)
-        dv[j] *= f.alpha;
+      for (int j = 0; j < 4; ++j) {
+        const f2 g = fma2(nc2, s[j], fma2(r2, mul2(dh[j], mul[j]), dv[j]));  // dv
+        const int i = 4 * k + j;
+        sa[i] = fma2(mul2(dh[j], s[j]), r2, sa[i]);
+        sb[i] = add2(sb[i], dh[j]);
+        sq[i] = fma2(g, mul2(y[j], rp2), sq[i]);
+        split2f(mul2(rp2, fma2(ncy2, y[j], mul2(g, w[j]))), o1[2 * j], o1[2 * j + 1]);  // (rp = 1, cy = 0 without the norm)
+        split2f(mul2(al2, g), o0[2 * j], o0[2 * j + 1]);
       }
       if (live) {
-        row_store<E>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, k, dv);
-        row_store<E>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, k, y);
+        row_store<E>(reinterpret_cast<RT*>(a.dx) + (size_t)m * D, D, t, tpr, k, o0);
+        row_store<E>(reinterpret_cast<CT*>(a.dy) + (size_t)m * D, D, t, tpr, k, o1);
       }
     }
     if (!KEEP) done();
   }
   if (!a.part) return;
   float* part = a.part + (size_t)blockIdx.x * 3 * D;
+  float fa[NV], fb[NV], fq[NV];
+#pragma unroll
+  for (int j = 0; j < NV / 2; ++j) {
+    split2f(sa[j], fa[2 * j], fa[2 * j + 1]);
+    split2f(sb[j], fb[2 * j], fb[2 * j + 1]);
+    split2f(sq[j], fq[2 * j], fq[2 * j + 1]);
+  }
   if (R == 1) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = elem<E>(t, tpr, j);
-      if (i < D) part[i] = sa[j], part[D + i] = sb[j], part[2 * D + i] = sq[j];
+      if (i < D) part[i] = fa[j], part[D + i] = fb[j], part[2 * D + i] = fq[j];
     }
     return;
   }
@@ -526,7 +579,7 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float* d = dyn + (size_t)ry * 3 * W + elem<E>(t, tpr, j);
-    d[0] = sa[j], d[W] = sb[j], d[2 * W] = sq[j];
+    d[0] = fa[j], d[W] = fb[j], d[2 * W] = fq[j];
   }
   row_bar(n);
   for (int i = threadIdx.x; i < 3 * D; i += n) {
