@@ -7,7 +7,9 @@
 // and the parameter gradients are column sums of dh n, dh and dv q.
 //
 // Bound by memory: forward 4, backward 6 row passes, each element read or
-// written once.  A producer warp keeps a ring of row groups filled with
+// written once (16896 x 1536, 1.965 GHz: 54.5 us, 0.87 of the copy rate; backward
+// 84.6 us, 0.84; rows of 1537, which have no vector accesses, are bound by issue:
+// 84 and 109 us).  A producer warp keeps a ring of row groups filled with
 // asynchronous bulk copies (rows are contiguous, so a group is one span per
 // matrix, widened to 16-byte granules: the ring takes any row length and
 // alignment, and costs the row threads no registers).  A row's threads hold
