@@ -324,6 +324,14 @@ def test_residual_norm_backward(M, per, D, r, t, post, gate, mod, gain, alpha):
     assert torch.equal(a, a2) and torch.equal(b, b2)
 
 
+@pytest.mark.parametrize("r,t", [(FP, BF), (BF, BF), (FP, FP)])
+@pytest.mark.parametrize("M,per,D", [(19, 7, 4001), (13, 5, 8191), (700, 350, 4001), (1, 0, 7681)])
+def test_residual_norm_wide_odd(M, per, D, r, t):
+    """Wide rows without vector accesses, 16 and 24 columns a thread, in every type: both directions."""
+    test_residual_norm(M, per, D, r, t, True, True, True, True, 0.75)
+    test_residual_norm_backward(M, per, D, r, t, True, True, True, True, 0.75)
+
+
 # ----------------------------------------------------------- more of each
 @pytest.mark.parametrize("M,N,K,o,res", [
     (300, 200, 2000, FP, True),    # a segmented reduction, ragged
