@@ -46,6 +46,7 @@
 #include "cluster.cuh"
 #include "kernels.h"
 #include "op_epilogue.cuh"
+#include "op_reduction.h"
 
 namespace wam {
 namespace {
@@ -73,6 +74,7 @@ struct ProductK {
   int M, N;           // N: columns of the output (gated: of g and of u each)
   int kb0, kb;        // k-blocks of the first operand pair, of all pairs
   int pieces;         // shares of the reduction, each a tile of its own with its own output
+  int chain;          // longest accumulator segment in k-blocks (0: one segment)
   int bn;             // accumulator columns of a tile (gated: g and u halves)
   int tiles_m, tiles_n, tile0;
   int a_mn, b_mn, gated;
@@ -86,7 +88,7 @@ struct GemmArgs {
   int subs;  // k-blocks of a full stage
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
   int nbuf, buf_cols;  // accumulator buffers
-  int nseg;            // segments of a tile's reduction
+  int nseg;            // fp32 operands: segment accumulators of the buffer
   int tm_cols;  // tensor-memory columns to allocate
 };
 
@@ -490,23 +492,23 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
   if (CG == 2) cluster_sync();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // Accumulator buffers.  A tile's reduction goes through nseg segments of up to
-  // seg_blocks k-blocks (the tensor core's additions truncate, which a long
-  // chain would show in an fp32 output): each fills a buffer of its own, and the
-  // epilogue warps add them up while the next one runs.  fp32 operands:
-  // the segments, and the small products, lie side by side in one.
+  // Accumulator buffers.  Where the output is fp32 a tile's reduction goes through
+  // segments (the tensor core's additions truncate, which a long chain would
+  // show): each fills a buffer of its own, and the epilogue warps add them up
+  // while the next one runs.  fp32 operands: the segments, and the small
+  // products, lie side by side in one.
   const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.buf_cols;
-  auto seg_blocks = [&](int n_kb) {  // (whole stages)
-    return ((n_kb + nseg - 1) / nseg + g.subs - 1) / g.subs * g.subs;
-  };
   pdl_trigger();
 
   // k-blocks of this CTA's part of a tile
   auto k_lo = [&](const ProductK& P, int piece) {
-    return S > 1 ? (int)((long long)P.kb * rank / S) : (int)((long long)P.kb * piece / P.pieces);
+    return S > 1 ? share_begin(P.kb, rank, S) : share_begin(P.kb, piece, P.pieces);
   };
   auto k_hi = [&](const ProductK& P, int piece) {
-    return S > 1 ? (int)((long long)P.kb * (rank + 1) / S) : (int)((long long)P.kb * (piece + 1) / P.pieces);
+    return S > 1 ? share_begin(P.kb, rank + 1, S) : share_begin(P.kb, piece + 1, P.pieces);
+  };
+  auto segments = [&](const ProductK& P, int lo, int hi) {
+    return segments_of(lo, hi, P.kb0, g.subs, P.chain, F32 ? nseg : 0);
   };
 
   if (warp == 0) {
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
               ok = false;
               break;
             }
-            const int ns = min(subs, end - kb);
+            const int ns = stage_blocks(kb, end, end, subs);
             // (a reduction-outermost box brings the rows of a whole stage)
             if (!peer)
               mbar_arrive_expect_tx(&full[st], (uint32_t)(kABytes * (amn ? subs : ns) + bbytes * (bmn ? subs : ns)) * CG);
@@ -602,9 +604,9 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const uint64_t da0 = smem_desc(0, amn, subs), db0 = smem_desc(0, bmn, subs);
         // bytes from one k-block of a stage to the next
         const uint32_t a_sub = amn ? 8192 : kABytes, b_sub = bmn ? 8192 : bn / CG * BK * 2;
-        const int lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece), kb0 = P.kb0, seg = seg_blocks(hi - lo);
+        const int lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece), kb0 = P.kb0, per = segments(P, lo, hi).per;
         uint32_t d = tmem + buf * buf_cols;
-        int in = 0;  // k-blocks in the present segment
+        int in = 0, segst = 0;  // k-blocks and stages in the present segment
         for (int kb = lo; kb < hi;) {
           if (!F32 && kb > lo && in == 0) {  // the next segment's buffer is drained
             if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) {
@@ -638,37 +640,38 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
             mma(1, 0, dx, 1);
             ++in, ++kb;
           } else {
-          const int ns = min(subs, (kb < kb0 ? min(hi, kb0) : hi) - kb);  // (a stage never spans two operand pairs)
-          uint32_t a0 = smem0 + (uint32_t)(st * sbytes), b0 = a0 + subs * kABytes;
-          for (int i = 0; i < ns; ++i, ++kb, a0 += a_sub, b0 += b_sub) {
-            // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
-            const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | (b0 >> 4 & 0x3FFF);
+            const int ns = stage_blocks(kb, hi, kb0, subs);
+            uint32_t a0 = smem0 + (uint32_t)(st * sbytes), b0 = a0 + subs * kABytes;
+            for (int i = 0; i < ns; ++i, ++kb, a0 += a_sub, b0 += b_sub) {
+              // (the address field is 14 bits: in a cluster, shared addresses carry the CTA's rank above them)
+              const uint64_t da = da0 | (a0 >> 4 & 0x3FFF), db = db0 | (b0 >> 4 & 0x3FFF);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
-              if constexpr (CG == 2)
-                tc_mma_bf16_pair(d, da + k * sa, db + k * sb, idesc, acc);
-              else
-                tc_mma_bf16(d, da + k * sa, db + k * sb, idesc, acc);
+              for (int k = 0; k < BK / 16; ++k) {
+                const uint32_t acc = (in > 0 || k > 0) ? 1u : 0u;
+                if constexpr (CG == 2)
+                  tc_mma_bf16_pair(d, da + k * sa, db + k * sb, idesc, acc);
+                else
+                  tc_mma_bf16(d, da + k * sa, db + k * sb, idesc, acc);
+              }
+              ++in;
             }
-            ++in;
           }
-          }
+          ++segst;
           if constexpr (CG == 2)
             tc_commit_both(smem_u32(&empty[st]));
           else
             tc_commit(&empty[st]);
           if (++st == stages) st = 0, phase ^= 1;
-          if (F32 ? kb >= hi : in >= seg || kb >= hi) {  // a buffer is complete
+          if (F32 ? kb >= hi : segst == per || kb >= hi) {  // a buffer is complete
             if constexpr (CG == 2)
               tc_commit_both(smem_u32(&accf[buf]));
             else
               tc_commit(&accf[buf]);
             if (++buf == nbuf) buf = 0, bphase ^= 1;
             ++lt;
-            in = 0;
-          } else if (F32 && in >= seg) {
-            in = 0, d += bn;
+            in = segst = 0;
+          } else if (F32 && segst == per) {
+            in = segst = 0, d += bn;
           }
         }
       }
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       const bool gated = P.gated;
       const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
       const int n0 = tl.n * (gated ? bn / 2 : bn);
-      const int n_kb = k_hi(P, tl.piece) - k_lo(P, tl.piece), sg = seg_blocks(n_kb), segs = (n_kb + sg - 1) / sg;
+      const int segs = segments(P, k_lo(P, tl.piece), k_hi(P, tl.piece)).count;
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       const int mw = m0 + quad * 32;
       auto ready = [&] {  // the present buffer is complete (one decision for all warps)
@@ -944,14 +947,16 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
   // ------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
+  // The epilogue has seen the last commit of every buffer.  After a wait that
+  // gave up it may not have: then the commits are waited for (again with a limit)
+  // before the tensor memory is freed.
   if (warp == 1) {
-    if (lane == 0) {  // the last commits have arrived before the tensor memory is freed
+    if (lane == 0 && *abort_flag) {
       int n = 0;
       for (int t = unit; t < g.tiles; t += units) {
         const Tile tl = tile_at(g, t);
         const ProductK& P = g.p[tl.p];
-        const int n_kb = k_hi(P, tl.piece) - k_lo(P, tl.piece), sg = seg_blocks(n_kb);
-        n += F32 ? 1 : (n_kb + sg - 1) / sg;
+        n += F32 ? 1 : segments(P, k_lo(P, tl.piece), k_hi(P, tl.piece)).count;
       }
       for (int l = max(0, n - nbuf); l < n; ++l)
         mbar_wait(&accf[l % nbuf], (l / nbuf) & 1, status, kStatusTimeoutDrain, nullptr);
@@ -1019,12 +1024,8 @@ cudaError_t device_info(Device** out) {
 
 struct Plan {
   int cg, bn, split;
-  int seg;  // accumulator segments
+  int seg;  // accumulator segments (the most of any product)
 };
-// Longest chain of k-blocks in one accumulator when the output is fp32: 896
-// products, about 9e-7 of the result in truncated additions (1536: 1.2e-6, 6144: 3e-6).
-constexpr int kChain = 14;
-constexpr int kChainF32 = 12;  // fp32 operands: 768
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Accumulator columns of product p's tiles under plan width bn.
@@ -1097,7 +1098,7 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
   for (int i = 0; i < n; ++i)
     if (mode == kF32 || p[i].e.out_f32) chain = std::max(chain, k_blocks(p[i]));
   auto consider = [&](Plan pl) {
-    pl.seg = std::max(1, ceil_div(ceil_div(chain, pl.split), mode == kF32 ? kChainF32 : kChain));
+    pl.seg = std::max(1, segments_for(ceil_div(chain, pl.split), mode == kF32 ? kChainF32 : kChain));
     if (mode != kF32) {
       if (pl.seg > 1 && pl.bn > 160) return;  // (two buffers and the sums: no tensor memory for wider tiles)
     } else if (pl.seg > 512 / pl.bn - 1) {  // no tensor memory for so many: the narrowest tile takes what there is
@@ -1176,6 +1177,7 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
     k.tiles_n = ceil_div(q.N, q.gated ? k.bn / 2 : k.bn);
     k.tile0 = tiles;
     k.pieces = std::max(1, q.pieces);
+    k.chain = mode == kF32 ? kChainF32 : q.e.out_f32 ? kChain : 0;
     tiles += k.tiles_m * k.tiles_n * k.pieces;
     k.a_mn = q.a_mn;
     k.b_mn = q.b_mn;

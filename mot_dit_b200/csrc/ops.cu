@@ -3,6 +3,7 @@
 #include <initializer_list>
 
 #include "kernels.h"
+#include "op_reduction.h"
 #include "wam.h"
 
 using namespace wam;
@@ -63,34 +64,6 @@ cudaError_t products(int dtype, const OpProduct* p, int n, const OpColSum* sums,
   return launch_op_gemm(p, n, dtype == WAM_FP32, sums, n_sums, s);
 }
 
-// Shares of the two gradients' reductions.  A gradient with few tiles and a
-// long reduction (the weights' of a narrow layer over many rows, the input's
-// of few rows through a wide one) would keep a few SMs busy after the rest are
-// done: its reduction is cut so that no tile takes longer than an SM's part
-// of all the work, at least `least` k-blocks each, and the pieces (fp32, in the
-// workspace) are added by a kernel after it.  linear 5128 rows, 271 x 74 fp32:
-// 149 us whole, 40 us in pieces.
-struct Pieces {
-  int dx, dw;
-};
-Pieces pieces_for(int dtype, int M, int N, int K, int sides) {
-  constexpr int kSms = 148;
-  const int bn = dtype == WAM_FP32 ? 64 : 128, least = dtype == WAM_FP32 ? 4 : 12;
-  const double over = dtype == WAM_FP32 ? 5 : 6;  // a tile's fixed part, in k-blocks
-  const double cols = (K + bn - 1) / bn;
-  const double tx = (M + 127) / 128 * cols, tw = sides * ((N + 127) / 128 * cols);
-  const int kx = sides * ((N + 63) / 64), kw = (M + 63) / 64;
-  const double share = (tx * (kx + over) + tw * (kw + over)) / kSms;
-  auto cut = [&](int kb, double elements) {
-    const double t = share > least ? share : least;
-    if (kb < 1.5 * t) return 1;
-    int p = (int)(kb / t + 0.999);
-    if (p > 16) p = 16;
-    while (p > 1 && p * elements * 4 > 32e6) --p;  // (the pieces stay in L2)
-    return p;
-  };
-  return {cut(kx, (double)M * K), cut(kw, (double)sides * N * K)};
-}
 // Workspace of a backward pass, in order: the activation's gradients (one or
 // two [M, N8] matrices of the compute type), the bias gradients' partial sums,
 // on the bf16 path when K is not a multiple of 8 copies of x and of the
@@ -114,7 +87,7 @@ BwdLayout bwd_layout(int dtype, int M, int N, int K, int sides, bool need_dz) {
   if (dtype == WAM_BF16 && K % 8) at += up((size_t)M * l.ldk * 2);
   l.w = at;
   if (dtype == WAM_BF16 && K % 8) at += sides * up((size_t)N * l.ldk * 2);
-  l.cut = pieces_for(dtype, M, N, K, sides);
+  l.cut = pieces_for(dtype == WAM_FP32, M, N, K, sides);
   l.px = at;
   if (l.cut.dx > 1) at += up((size_t)l.cut.dx * M * K * 4);
   l.pw = at;

@@ -1,0 +1,48 @@
+"""How the feed-forward products cut their reductions, on the host: the
+functions that every warp of the kernel counts by, replayed warp by warp."""
+import ctypes as C
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def replay(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("replay") / "replay.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", os.path.join(ROOT, "mot_dit_b200", "csrc"),
+                    os.path.join(ROOT, "tests", "c_abi", "reduction_replay.cpp"), "-o", out], check=True)
+    return C.CDLL(out)
+
+
+@pytest.mark.parametrize("subs", [1, 2])
+@pytest.mark.parametrize("chain", [0, 12, 14])
+def test_segments_of_any_part(replay, subs, chain):
+    """Parts of every length, with and without a seam between operand pairs in them."""
+    for n in range(1, 200):
+        for seam in [0, n, *range(1, n, 1 if n < 60 else 7)]:
+            lo = 3
+            assert replay.replay_part(lo, lo + n, lo + seam, subs, chain, 0) == 0, (n, seam)
+            assert replay.replay_part(lo, lo + n, lo + seam, subs, chain, 7) == 0, (n, seam)
+
+
+@pytest.mark.parametrize("sides", [1, 2])
+@pytest.mark.parametrize("f32", [0, 1])
+def test_segments_of_every_width(replay, f32, sides):
+    """The MMA warp closes as many accumulator segments as the epilogue waits for, at every width of a layer (with two
+    operand pairs, a piece that crosses the seam after an odd number of k-blocks had one segment fewer)."""
+    rows = (1, 16, 64, 256, 640, 2048, 8448)
+    for N in range(64, 32769, 64):  # (the counts go by k-blocks of 64)
+        for K in (64, 256, 512, 1024, 1536, 2048, 4096):
+            for M in rows:
+                assert replay.replay_backward(f32, M, N, K, sides) == 0, (M, N, K)
+
+
+@pytest.mark.parametrize("M,F,K", [(256, 8192, 1024), (16, 8192, 1536), (128, 8192, 1536), (64, 8192, 2048), (2048, 8192, 256)])
+def test_widths_that_a_seam_cuts(replay, M, F, K):
+    """Shapes whose input gradient is cut into three pieces, the middle one across the seam."""
+    assert replay.pieces_dx(0, M, F, K, 2) == 3
+    kb0 = F // 64
+    assert replay.replay_part(2 * kb0 // 3, 4 * kb0 // 3, kb0, 2, 14, 0) == 0

@@ -376,6 +376,30 @@ def test_gradients_in_pieces(M, N, K, t):
     T.within(outs[0], dx64, ex), T.within(outs[1], g64, eg), T.within(outs[2], u64, eu)
 
 
+@pytest.mark.parametrize("M,F,K", [(256, 8192, 1024), (16, 8192, 1536), (64, 8192, 2048), (640, 10816, 512), (2048, 13568, 64),
+                                   (70, 8127, 1030)])
+def test_gated_backward_across_the_seam(M, F, K):
+    """The input gradient sums over two operand pairs in pieces, one of which crosses from the first to the second after
+    an odd number of k-blocks: alone and with the other gradients."""
+    n = T.normals(M + 3 * F + K)
+    x, wg, wu = n(M, K, dtype=BF), n(F, K, std=K ** -0.5, dtype=BF), n(F, K, std=K ** -0.5, dtype=BF)
+    g, u, da = n(M, F, dtype=BF, std=1.5), n(M, F, dtype=BF), n(M, F, dtype=BF)
+    outs = [T.guarded(s, d) for s, d in (((M, K), BF), ((F, K), BF), ((F, K), BF), ((F,), FP), ((F,), FP))]
+    dx, dwg, dwu, dbg, dbu = (o[0] for o in outs)
+    ws = _ws(W.op_gated_workspace(W.BF16, M, F, K))
+    (dx64, ex), [((g64, eg), (bg64, ebg)), ((u64, eu), (bu64, ebu))] = T.gated_grad64(x, wg, wu, g, u, da, "silu")
+    W.op_gated_backward(W.BF16, x, wg, wu, g, u, da, dx, None, None, M, F, K, workspace=ws)
+    T.within(dx, dx64, ex)
+    alone = dx.clone()
+    W.op_gated_backward(W.BF16, x, wg, wu, g, u, da, dx, dwg, dwu, M, F, K, dbias_g=dbg, dbias_u=dbu, workspace=ws)
+    T.within(dx, dx64, ex), T.within(dwg, g64, eg), T.within(dwu, u64, eu)
+    T.within(dbg, bg64, ebg), T.within(dbu, bu64, ebu)
+    T.within(alone, dx64, ex)
+    for _, ok in outs:
+        ok()
+    W.ops_check_status()
+
+
 @pytest.mark.parametrize("t", [BF, FP])
 def test_backward_unaligned(t):
     """Every operand of the backward passes off a 16-byte boundary, one by one and together."""
