@@ -1029,11 +1029,8 @@ struct Plan {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Accumulator columns of product p's tiles under plan width bn.
-int tile_cols(const OpProduct& p, const Plan& pl) {
-  // (an MN-major operand comes in boxes of 64 columns, in halves to a pair; a gated tile's halves in 32s)
-  const int q = pl.cg == 2 ? 128 : p.b_mn || p.gated ? 64 : 32;
-  const int n = p.gated ? 2 * ceil_div(p.N, 32) * 32 : p.N;
-  return std::min(pl.bn, ceil_div(n, q) * q);
+int tile_cols(const OpProduct& p, const Plan& pl, int mode) {
+  return tile_columns(pl.bn, p.N, p.gated, p.b_mn, pl.cg == 2, mode == kF32);
 }
 int pieces_of(const OpProduct& p) { return std::max(1, p.pieces); }
 // k-blocks of one of its tiles (the longest piece's)
@@ -1053,7 +1050,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   const double tail = 11.0 * pl.bn + 600 + (pl.cg == 2 ? 1000 : 0);
   if (pl.split > 1) {
     const OpProduct& q = p[0];
-    const int bn = tile_cols(q, pl), tn = ceil_div(q.gated ? 2 * q.N : q.N, bn), tm = ceil_div(q.M, BM);
+    const int bn = tile_cols(q, pl, mode), tn = ceil_div(q.gated ? 2 * q.N : q.N, bn), tm = ceil_div(q.M, BM);
     const int waves = ceil_div(tm * tn, d.clusters[pl.split]);
     return waves * (ceil_div(k_blocks(q), pl.split) * per(q) + tail + 2500);
   }
@@ -1061,7 +1058,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   const bool bare = mode == kF32;  // one accumulator buffer: every tile's epilogue stands alone
   const double extra = bare ? tail : 150;
   if (n == 1) {
-    const int bn = tile_cols(p[0], pl), cols = p[0].gated ? 2 * p[0].N : p[0].N;
+    const int bn = tile_cols(p[0], pl, mode), cols = p[0].gated ? 2 * p[0].N : p[0].N;
     const long long tiles = (long long)ceil_div(p[0].M, BM * pl.cg) * ceil_div(cols, bn) * pieces_of(p[0]);
     return (double)((tiles + units - 1) / units) * (k_blocks(p[0]) * per(p[0]) + extra) + tail;
   }
@@ -1072,7 +1069,7 @@ double plan_cost(const OpProduct* p, int n, const Plan& pl, const Device& d, int
   double c[kOpProducts];
   for (int i = 0; i < n; ++i) {
     const long long tiles = (long long)ceil_div(p[i].M, BM * pl.cg) *
-                            ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl)) * pieces_of(p[i]);
+                            ceil_div(p[i].gated ? 2 * p[i].N : p[i].N, tile_cols(p[i], pl, mode)) * pieces_of(p[i]);
     c[i] = k_blocks(p[i]) * per(p[i]) + extra;
     first[i] = (int)(pos % units);
     whole[i] = tiles / units;
@@ -1117,7 +1114,7 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
     if ((bn & (bn - 1)) && (!narrow || mode == kF32)) continue;
     consider(Plan{1, bn, 1, 1});
     if (n > 1 || pieces_of(p[0]) > 1) continue;
-    const int cols = tile_cols(p[0], Plan{1, bn, 1, 1});
+    const int cols = tile_cols(p[0], Plan{1, bn, 1, 1}, mode);
     const long long tiles = (long long)ceil_div(p[0].M, BM) * ceil_div(p[0].gated ? 2 * p[0].N : p[0].N, cols);
     for (int s = 2; s <= 8; ++s)
       if (tiles <= d.clusters[s] && k_blocks(p[0]) >= 2 * s) consider(Plan{1, bn, s, 1});
@@ -1156,7 +1153,7 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
   const Plan pl = choose(p, n, mode, *d);
   GemmArgs g;
   int bmax = 0;
-  for (int i = 0; i < n; ++i) bmax = std::max(bmax, tile_cols(p[i], pl));
+  for (int i = 0; i < n; ++i) bmax = std::max(bmax, tile_cols(p[i], pl, mode));
   const int sub_bytes = (kABytes + bmax / pl.cg * BK * 2) * (f32 ? 3 : 1), room = kSmemMax - kBarBytes - kEpiWarps * kStg;
   g.subs = mode == kTma && 6 * sub_bytes <= room ? 2 : 1;
   g.stage_bytes = g.subs * sub_bytes;
@@ -1172,7 +1169,7 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
     k.N = q.N;
     k.kb = std::max(1, q.pairs) * ceil_div(q.K, BK);
     k.kb0 = ceil_div(q.K, BK);
-    k.bn = tile_cols(q, pl);
+    k.bn = tile_cols(q, pl, mode);
     k.tiles_m = ceil_div(q.M, BM * pl.cg);
     k.tiles_n = ceil_div(q.N, q.gated ? k.bn / 2 : k.bn);
     k.tile0 = tiles;

@@ -1,7 +1,8 @@
-// How the reduction of a feed-forward product is cut (host and device, plain
-// integers): into pieces that are tiles of their own, into the stages of the
-// operand ring, and into the segments of an accumulator.  Every warp of a CTA
-// counts stages and segments by these functions, and by nothing else.
+// How a feed-forward product is cut (host and device, plain integers): its
+// columns into tiles, its reduction into pieces that are tiles of their own, into
+// the stages of the operand ring, and into the segments of an accumulator.
+// Every warp of a CTA counts stages and segments by these functions, and by
+// nothing else.
 #pragma once
 
 #ifdef __CUDACC__
@@ -39,6 +40,17 @@ inline Pieces pieces_for(bool f32, int M, int N, int K, int sides) {
     return p;
   };
   return {cut(kx, (double)M * K), cut(kw, (double)sides * N * K)};
+}
+// Accumulator columns of the tiles of a product with N output columns (gated: of
+// g and of u each) whose plan asks for bn: no more than N needs.  They come in
+// steps of 32, which a box of a matrix with the reduction innermost can have;
+// of 64, the box of a reduction-outermost one (b_mn), the halves of a gated tile
+// and the widths that the loaders of fp32 operands are made for; of 128 to a
+// pair, in halves.
+inline int tile_columns(int bn, int N, bool gated, bool b_mn, bool pair, bool f32) {
+  const int step = pair ? 128 : b_mn || gated || f32 ? 64 : 32;
+  const int n = gated ? 2 * ((N + 31) / 32 * 32) : N, cols = (n + step - 1) / step * step;
+  return cols < bn ? cols : bn;
 }
 // First k-block of share i of n (at most 16) of a reduction of kb k-blocks (at
 // most 2^19: two pairs of the longest one).

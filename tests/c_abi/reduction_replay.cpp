@@ -53,3 +53,4 @@ extern "C" int replay_backward(int f32, int M, int N, int K, int sides) {
   return 0;
 }
 extern "C" int pieces_dx(int f32, int M, int N, int K, int sides) { return pieces_for(f32, M, N, K, sides).dx; }
+extern "C" int columns(int bn, int N, int gated, int b_mn, int pair, int f32) { return tile_columns(bn, N, gated, b_mn, pair, f32); }

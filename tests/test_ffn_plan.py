@@ -46,3 +46,21 @@ def test_widths_that_a_seam_cuts(replay, M, F, K):
     assert replay.pieces_dx(0, M, F, K, 2) == 3
     kb0 = F // 64
     assert replay.replay_part(2 * kb0 // 3, 4 * kb0 // 3, kb0, 2, 14, 0) == 0
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("b_mn", [0, 1])
+def test_tile_widths(replay, gated, b_mn):
+    """fp32 tiles are as wide as one of the two loaders (a linear layer of up to 32 or of 65 to 96 columns had tiles of 32
+    or 96, which neither brings in); the others are whole boxes."""
+    for N in range(1, 400):
+        need = 2 * ((N + 31) // 32 * 32) if gated else N
+        for bn in (64, 128):
+            c = replay.columns(bn, N, gated, b_mn, 0, 1)
+            assert c in (64, 128) and c <= bn and (c == bn or c >= need), (N, bn, c)
+        for bn in range(64, 257, 32):
+            c = replay.columns(bn, N, gated, b_mn, 0, 0)
+            assert c <= bn and c % (64 if (gated or b_mn) and bn % 64 == 0 else 32) == 0 and (c == bn or need <= c < need + 64)
+        for bn in (128, 192, 256):
+            c = replay.columns(bn, N, gated, b_mn, 1, 0)
+            assert c <= bn and c % 64 == 0 and (c == bn or need <= c < need + 128)

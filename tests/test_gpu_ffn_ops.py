@@ -355,6 +355,25 @@ def test_linear_forms(M, N, K, o, res):
         assert ((y.double() - y64).norm() / y64.norm()).item() < 1e-6
 
 
+@pytest.mark.parametrize("N", [1, 8, 31, 32, 33, 64, 65, 80, 95, 96, 97, 128, 160])
+def test_linear_fp32_narrow(N):
+    """fp32 layers with fewer columns than a tile, at few rows and many."""
+    for M, K in ((9, 200), (140, 67), (1000, 320), (40, 1536)):
+        n = T.normals(M + N + K)
+        x, w, b, r = n(M, K), n(N, K, std=K ** -0.5), n(N), n(M, N)
+        (y, ok1), (z, ok2) = T.guarded((M, N), FP), T.guarded((M, N), FP)
+        W.op_linear_act(W.FP32, x, w, b, y, M, N, K, act=ACT["silu"], residual=r, z=z)
+        z64, ez, y64, ey = T.linear64(x, w, b, r, "silu", FP)
+        T.within(y, y64, ey), T.within(z, z64, ez)
+        ok1(), ok2()
+        (dx, ok1), (dw, ok2), db = T.guarded((M, K), FP), T.guarded((N, K), FP), torch.empty(N, device="cuda")
+        W.op_linear_act_backward(W.FP32, x, w, z, r, dx, dw, db, M, N, K, act=ACT["silu"],
+                                 workspace=_ws(W.op_linear_act_workspace(W.FP32, M, N, K, act=ACT["silu"])))
+        (dx64, ex), [((dw64, ew), (db64, eb))] = T.linear_grad64(x, w, z, r, "silu")
+        T.within(dx, dx64, ex), T.within(dw, dw64, ew), T.within(db, db64, eb)
+        ok1(), ok2()
+
+
 @pytest.mark.parametrize("M,N,K,t", [(9000, 100, 72, BF), (9000, 70, 130, BF), (40, 5000, 200, BF), (5128, 271, 74, FP), (43, 3000, 520, FP)])
 def test_gradients_in_pieces(M, N, K, t):
     """Few tiles and a long reduction: it is cut into pieces that are added afterwards."""
