@@ -88,7 +88,7 @@ struct GemmArgs {
   int subs;  // k-blocks of a full stage
   int split;    // CTAs of a cluster that share one tile's reduction (1: persistent)
   int nbuf, buf_cols;  // accumulator buffers
-  int nseg;            // fp32 operands: segment accumulators of the buffer
+  int nseg;            // fp32 operands: segment accumulators of the buffer (a round)
   int tm_cols;  // tensor-memory columns to allocate
 };
 
@@ -495,8 +495,9 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
   // Accumulator buffers.  Where the output is fp32 a tile's reduction goes through
   // segments (the tensor core's additions truncate, which a long chain would
   // show): each fills a buffer of its own, and the epilogue warps add them up
-  // while the next one runs.  fp32 operands: the segments, and the small
-  // products, lie side by side in one.
+  // while the next one runs.  fp32 operands: up to nseg segments, and the small
+  // products, lie side by side in one; a longer reduction takes several such
+  // rounds, added up the same way.
   const int nbuf = g.nbuf, nseg = g.nseg, buf_cols = g.buf_cols;
   pdl_trigger();
 
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
     return S > 1 ? share_begin(P.kb, rank + 1, S) : share_begin(P.kb, piece + 1, P.pieces);
   };
   auto segments = [&](const ProductK& P, int lo, int hi) {
-    return segments_of(lo, hi, P.kb0, g.subs, P.chain, F32 ? nseg : 0);
+    return segments_of(lo, hi, P.kb0, g.subs, P.chain);
   };
 
   if (warp == 0) {
@@ -607,8 +608,9 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         const int lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece), kb0 = P.kb0, per = segments(P, lo, hi).per;
         uint32_t d = tmem + buf * buf_cols;
         int in = 0, segst = 0;  // k-blocks and stages in the present segment
+        int slot = 0;           // fp32 operands: the segment's place in its round
         for (int kb = lo; kb < hi;) {
-          if (!F32 && kb > lo && in == 0) {  // the next segment's buffer is drained
+          if (kb > lo && in == 0 && slot == 0) {  // the next segment's (round's) buffer is drained
             if (lt >= nbuf && !mbar_wait(&acce[buf], bphase ^ 1, status, kStatusTimeoutAccum, abort_flag)) {
               ok = false;
               break;
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
               for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(to, da + k * sa, db + k * sb, idesc, k > 0 ? 1u : acc0);
             };
             mma(0, 0, d, in > 0);
-            mma(0, 2, dx, kb > lo);
+            mma(0, 2, dx, in > 0 || slot > 0);
             mma(2, 0, dx, 1);
             mma(1, 1, dx, 1);
             mma(0, 1, dx, 1);
@@ -662,16 +664,24 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
           else
             tc_commit(&empty[st]);
           if (++st == stages) st = 0, phase ^= 1;
-          if (F32 ? kb >= hi : segst == per || kb >= hi) {  // a buffer is complete
+          bool last = kb >= hi;  // of the buffer
+          if (segst == per) {
+            in = segst = 0;
+            if constexpr (F32) {
+              d += bn;
+              last |= ++slot == nseg;
+            } else {
+              last = true;
+            }
+          }
+          if (last) {
             if constexpr (CG == 2)
               tc_commit_both(smem_u32(&accf[buf]));
             else
               tc_commit(&accf[buf]);
             if (++buf == nbuf) buf = 0, bphase ^= 1;
             ++lt;
-            in = segst = 0;
-          } else if (F32 && segst == per) {
-            in = segst = 0, d += bn;
+            in = segst = slot = 0;
           }
         }
       }
@@ -697,31 +707,14 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
     for (int t = unit; t < g.tiles; t += units) {
       const Tile tl = tile_at(g, t);
       const ProductK& P = g.p[tl.p];
-      if constexpr (F32) {  // these warps bring the operands in first
-        const bool va = vec_f32(P.a[0]) && vec_f32(P.a[1]), vb = vec_f32(P.b[0]) && vec_f32(P.b[1]);
-        const int m0_ = tl.m * BM, n0_ = tl.n * (P.gated ? P.bn / 2 : P.bn), lo = k_lo(P, tl.piece), hi = k_hi(P, tl.piece);
-#define WAM_FEED(BN, VA, VB) \
-  feed_f32<BN, VA, VB>(P, m0_, n0_, lo, hi, te, smem, sbytes, stages, full, empty, feed, status, abort_flag)
-        if (P.bn == 128) {
-          if (va)
-            vb ? WAM_FEED(128, true, true) : WAM_FEED(128, true, false);
-          else
-            vb ? WAM_FEED(128, false, true) : WAM_FEED(128, false, false);
-        } else {
-          if (va)
-            vb ? WAM_FEED(64, true, true) : WAM_FEED(64, true, false);
-          else
-            vb ? WAM_FEED(64, false, true) : WAM_FEED(64, false, false);
-        }
-#undef WAM_FEED
-      }
       OpEpi e = P.e;
       if (tl.piece) e.out = reinterpret_cast<float*>(e.out) + (size_t)tl.piece * P.M * e.ld;
       const int bn = P.bn, pM = P.M, pN = P.N;
       const bool gated = P.gated;
       const int m0 = (tl.m * CG + (CG == 2 ? (int)rank : 0)) * BM;
       const int n0 = tl.n * (gated ? bn / 2 : bn);
-      const int segs = segments(P, k_lo(P, tl.piece), k_hi(P, tl.piece)).count;
+      const int k_first = k_lo(P, tl.piece), k_end = k_hi(P, tl.piece);
+      const Segments sg = segments(P, k_first, k_end);
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
       const int mw = m0 + quad * 32;
       auto ready = [&] {  // the present buffer is complete (one decision for all warps)
@@ -741,53 +734,65 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
             mbar_arrive(&acce[buf]);
         }
       };
-      // segments but the last: summed in tensor memory, behind the buffers (in
-      // registers the sums took those of the rest of the epilogue)
-      const uint32_t t_sum = t_lane + nbuf * buf_cols;
-      bool stop = false;
-      if constexpr (!F32) {
-        for (int k = 0; k + 1 < segs; ++k) {
-          stop = !ready();
-          if (stop) break;
-#pragma unroll 1
-          for (int c = 32 * half; c < bn; c += 64) {
-            float w[32];
-            tmem_ld32(t_lane + buf * buf_cols + c, w);
-            if (k > 0) {
-              float x[32];
-              tmem_ld32(t_sum + c, x);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) w[j] += x[j];
-            }
-            tmem_st32f(t_sum + c, w);
-          }
-          drained();
-          if (++buf == nbuf) buf = 0, bphase ^= 1;
-        }
-      }
-      if (stop || !ready()) break;
-      const uint32_t t_row = t_lane + buf * buf_cols;
-      // 32 accumulator columns, the segments added
-      auto acc32 = [&](int c, float (&v)[32]) {
+      // all but the last segment (fp32 operands: round): summed in tensor memory,
+      // behind the buffers (in registers the sums took those of the rest of the
+      // epilogue)
+      const uint32_t t_sum = t_lane + (F32 ? (nseg + 1) * bn : nbuf * buf_cols);
+      const int fills = F32 ? (sg.count + nseg - 1) / nseg : sg.count;  // of a buffer
+      int held = 1;  // segments in the present buffer
+      // 32 columns of the present buffer, with those of the buffers before
+      auto acc32 = [&](int c, bool before, float (&v)[32]) {
+        const uint32_t t_row = t_lane + buf * buf_cols;
+        float w[32];
         tmem_ld32(t_row + c, v);
         if constexpr (F32) {
-          float w[32];
-          tmem_ld32(t_row + nseg * bn + c, w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += w[i];
 #pragma unroll 1
-          for (int k = 1; k < segs; ++k) {
-            tmem_ld32(t_row + k * bn + c, w);
+          for (int k = 0; k < held; ++k) {  // the small products, the other segments
+            tmem_ld32(t_row + (k ? k : nseg) * bn + c, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] += w[i];
           }
-        } else if (segs > 1) {
-          float w[32];
+        }
+        if (before) {
           tmem_ld32(t_sum + c, w);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] += w[i];
         }
       };
+      bool stop = false;
+      for (int k = 0;; ++k) {
+        if constexpr (F32) {  // these warps bring the operands in first
+          held = min(nseg, sg.count - k * nseg);
+          const bool va = vec_f32(P.a[0]) && vec_f32(P.a[1]), vb = vec_f32(P.b[0]) && vec_f32(P.b[1]);
+          const int lo = k_first + k * nseg * sg.per, hi = min(k_end, lo + nseg * sg.per);
+#define WAM_FEED(BN, VA, VB) \
+  feed_f32<BN, VA, VB>(P, m0, n0, lo, hi, te, smem, sbytes, stages, full, empty, feed, status, abort_flag)
+          if (bn == 128) {
+            if (va)
+              vb ? WAM_FEED(128, true, true) : WAM_FEED(128, true, false);
+            else
+              vb ? WAM_FEED(128, false, true) : WAM_FEED(128, false, false);
+          } else {
+            if (va)
+              vb ? WAM_FEED(64, true, true) : WAM_FEED(64, true, false);
+            else
+              vb ? WAM_FEED(64, false, true) : WAM_FEED(64, false, false);
+          }
+#undef WAM_FEED
+        }
+        stop = !ready();
+        if (stop || k + 1 == fills) break;
+#pragma unroll 1
+        for (int c = 32 * half; c < bn; c += 64) {
+          float w[32];
+          acc32(c, k > 0, w);
+          tmem_st32f(t_sum + c, w);
+        }
+        drained();
+        if (++buf == nbuf) buf = 0, bphase ^= 1;
+      }
+      if (stop) break;
+      const uint32_t t_row = t_lane + buf * buf_cols;
       if (S > 1) {
         // leave the partial tile in the idle operand ring, chunk q of row r at q ^ (r & 7)
         if (mw < pM) {
@@ -795,7 +800,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
           uint8_t* row = smem + (size_t)r * bn * 4;
           for (int c = 32 * half; c < bn; c += 64) {
             float v[32];
-            acc32(c, v);
+            acc32(c, fills > 1, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               *reinterpret_cast<float4*>(row + ((((c >> 2) + q) ^ (r & 7)) << 4)) =
@@ -815,8 +820,8 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
         if (gated) {
           float u[32];
           if constexpr (F32) {
-            acc32(c, v);
-            acc32(bn / 2 + c, u);
+            acc32(c, fills > 1, v);
+            acc32(bn / 2 + c, fills > 1, u);
           } else {  // (its output is never fp32: one segment)
             tmem_ld32(t_row + c, v);
             tmem_ld32(t_row + bn / 2 + c, u);
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
             else
               rv.load<__nv_bfloat16>(e.res, w, lane);
           }
-          acc32(c, v);
+          acc32(c, fills > 1, v);
           if (c + 64 >= width) drained();
           if (!live) continue;
           add_bias(v, e.bias, w.n0, pN, e.vec);
@@ -956,7 +961,8 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       for (int t = unit; t < g.tiles; t += units) {
         const Tile tl = tile_at(g, t);
         const ProductK& P = g.p[tl.p];
-        n += F32 ? 1 : segments(P, k_lo(P, tl.piece), k_hi(P, tl.piece)).count;
+        const int segs = segments(P, k_lo(P, tl.piece), k_hi(P, tl.piece)).count;
+        n += F32 ? (segs + nseg - 1) / nseg : segs;
       }
       for (int l = max(0, n - nbuf); l < n; ++l)
         mbar_wait(&accf[l % nbuf], (l / nbuf) & 1, status, kStatusTimeoutDrain, nullptr);
@@ -1025,6 +1031,7 @@ cudaError_t device_info(Device** out) {
 struct Plan {
   int cg, bn, split;
   int seg;  // accumulator segments (the most of any product)
+  int sum = 0;  // fp32 operands: the segments come in rounds of seg, which are added up
 };
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -1098,9 +1105,10 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
     pl.seg = std::max(1, segments_for(ceil_div(chain, pl.split), mode == kF32 ? kChainF32 : kChain));
     if (mode != kF32) {
       if (pl.seg > 1 && pl.bn > 160) return;  // (two buffers and the sums: no tensor memory for wider tiles)
-    } else if (pl.seg > 512 / pl.bn - 1) {  // no tensor memory for so many: the narrowest tile takes what there is
+    } else if (pl.seg > 512 / pl.bn - 1) {  // no tensor memory for so many: rounds, on the narrowest tile
       if (pl.bn > 64) return;
-      pl.seg = 512 / pl.bn - 1;
+      pl.seg = 512 / pl.bn - 2;
+      pl.sum = 1;
     }
     const double c = plan_cost(p, n, pl, d, mode);
     if (c < bc) bc = c, best = pl;
@@ -1198,7 +1206,7 @@ cudaError_t launch_op_gemm(const OpProduct* p, int n, bool f32, const OpColSum* 
   g.nbuf = f32 ? 1 : 2;
   g.tm_cols = 32;
   g.buf_cols = bmax;
-  while (g.tm_cols < (f32 ? pl.seg + 1 : pl.seg > 1 ? 3 : 2) * bmax) g.tm_cols *= 2;
+  while (g.tm_cols < (f32 ? pl.seg + 1 + pl.sum : pl.seg > 1 ? 3 : 2) * bmax) g.tm_cols *= 2;
   const size_t smem = (size_t)g.stages * g.stage_bytes + kEpiWarps * kStg + kBarBytes;
 
   const int cluster = pl.cg == 2 ? 2 : pl.split;

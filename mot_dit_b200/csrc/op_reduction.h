@@ -74,16 +74,15 @@ WAM_HD int stages_of(int lo, int hi, int kb0, int subs) {
   return ((seam - lo + subs - 1) >> (subs - 1)) + ((hi - seam + subs - 1) >> (subs - 1));
 }
 // Accumulator segments of a part of n k-blocks whose chains are at most
-// `chain` long (0: any length; a short stage may shift a block between two).
+// `chain` long (0: any length; a seam in the part may make them a stage longer).
 WAM_HD int segments_for(int n, int chain) { return chain ? (n + chain - 1) / chain : 1; }
 // The segments of the k-blocks [lo, hi): whole stages, `per` each but the last.
 struct Segments {
   int per, count;
 };
-WAM_HD Segments segments_of(int lo, int hi, int kb0, int subs, int chain, int most) {
+WAM_HD Segments segments_of(int lo, int hi, int kb0, int subs, int chain) {
   const int stages = stages_of(lo, hi, kb0, subs);
-  int n = segments_for(hi - lo, chain);
-  if (most && n > most) n = most;
+  const int n = segments_for(hi - lo, chain);
   if (n <= 1) return {stages, 1};
   Segments s;
   s.per = (stages + n - 1) / n;

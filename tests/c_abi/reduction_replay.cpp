@@ -8,35 +8,44 @@
 
 using namespace wam;
 
-extern "C" int replay_part(int lo, int hi, int kb0, int subs, int chain, int most) {
-  const Segments sg = segments_of(lo, hi, kb0, subs, chain, most);
+extern "C" int replay_part(int lo, int hi, int kb0, int subs, int chain, int nseg) {  // nseg: fp32 operands, segments a round (else 0)
+  const Segments sg = segments_of(lo, hi, kb0, subs, chain);
   if (sg.per < 1 || sg.count < 1 || sg.count > std::max(1, segments_for(hi - lo, chain))) return 1;
-  if (most && sg.count > most) return 2;
-  // the producer's stages, one operand pair after the other
-  int starts[2048], n = 0;
-  for (int q = 0; q < 2; ++q) {
-    const int end = q ? hi : std::min(hi, kb0);
-    for (int kb = q ? std::max(lo, kb0) : lo; kb < end;) {
-      if (n == 2048) return 3;
-      starts[n++] = kb;
-      kb += stage_blocks(kb, end, end, subs);
+  const int fills = nseg ? (sg.count + nseg - 1) / nseg : sg.count;
+  // the producer's stages, one operand pair after the other (fp32: round after round)
+  int starts[4096], n = 0;
+  if (nseg) {
+    for (int k = 0; k < fills; ++k)
+      for (int kb = lo + k * nseg * sg.per; kb < std::min(hi, lo + (k + 1) * nseg * sg.per); ++kb) {
+        if (n == 4096) return 3;
+        starts[n++] = kb;
+      }
+  } else {
+    for (int q = 0; q < 2; ++q) {
+      const int end = q ? hi : std::min(hi, kb0);
+      for (int kb = q ? std::max(lo, kb0) : lo; kb < end;) {
+        if (n == 4096) return 3;
+        starts[n++] = kb;
+        kb += stage_blocks(kb, end, end, subs);
+      }
     }
   }
   if (n != stages_of(lo, hi, kb0, subs)) return 4;
   // the MMA warp
-  int st = 0, in = 0, closed = 0, blocks = 0;
+  int st = 0, in = 0, slot = 0, closed = 0, blocks = 0;
   for (int kb = lo; kb < hi;) {
     if (st == n || starts[st] != kb) return 5;
+    if (nseg && in == 0 && slot == 0 && kb != lo + closed * nseg * sg.per) return 2;
     const int ns = stage_blocks(kb, hi, kb0, subs);
     if (ns < 1 || ns > subs || (kb < kb0 && kb + ns > kb0)) return 6;
     kb += ns, ++st, ++in, blocks += ns;
-    if (in == sg.per || kb >= hi) {
-      if (chain && !most && blocks > (chain + subs - 1) / subs * subs + subs) return 7;  // (a seam may add one stage)
-      ++closed, in = blocks = 0;
-    }
+    if (chain && blocks > (chain + subs - 1) / subs * subs + (lo < kb0 && kb0 < hi ? subs : 0)) return 7;  // (a seam may add a stage)
+    bool last = kb >= hi;
+    if (in == sg.per) in = blocks = 0, last |= !nseg || ++slot == nseg;
+    if (last) ++closed, in = blocks = slot = 0;
   }
   if (st != n) return 8;
-  return closed == sg.count ? 0 : 9;
+  return closed == fills ? 0 : 9;
 }
 // Every piece of a backward pass's two reductions, at one and two k-blocks a stage.
 extern "C" int replay_backward(int f32, int M, int N, int K, int sides) {
@@ -45,12 +54,13 @@ extern "C" int replay_backward(int f32, int M, int N, int K, int sides) {
   for (int subs = 1; subs <= (f32 ? 1 : 2); ++subs)
     for (int chain : {0, f32 ? kChainF32 : kChain}) {
       for (int i = 0; i < c.dx; ++i)
-        if (int e = replay_part(share_begin(sides * kx, i, c.dx), share_begin(sides * kx, i + 1, c.dx), kx, subs, chain, f32 ? 7 : 0))
+        if (int e = replay_part(share_begin(sides * kx, i, c.dx), share_begin(sides * kx, i + 1, c.dx), kx, subs, chain, f32 ? 6 : 0))
           return 100 + e;
       for (int i = 0; i < c.dw; ++i)
-        if (int e = replay_part(share_begin(kw, i, c.dw), share_begin(kw, i + 1, c.dw), kw, subs, chain, f32 ? 7 : 0)) return 200 + e;
+        if (int e = replay_part(share_begin(kw, i, c.dw), share_begin(kw, i + 1, c.dw), kw, subs, chain, f32 ? 6 : 0)) return 200 + e;
     }
   return 0;
 }
 extern "C" int pieces_dx(int f32, int M, int N, int K, int sides) { return pieces_for(f32, M, N, K, sides).dx; }
 extern "C" int columns(int bn, int N, int gated, int b_mn, int pair, int f32) { return tile_columns(bn, N, gated, b_mn, pair, f32); }
+extern "C" int longest_chain(int n, int subs, int chain) { return std::min(n, segments_of(0, n, n, subs, chain).per * subs); }

@@ -25,7 +25,8 @@ def test_segments_of_any_part(replay, subs, chain):
         for seam in [0, n, *range(1, n, 1 if n < 60 else 7)]:
             lo = 3
             assert replay.replay_part(lo, lo + n, lo + seam, subs, chain, 0) == 0, (n, seam)
-            assert replay.replay_part(lo, lo + n, lo + seam, subs, chain, 7) == 0, (n, seam)
+            for nseg in (1, 3, 6) if subs == 1 else ():  # fp32 operands: rounds of segments
+                assert replay.replay_part(lo, lo + n, lo + seam, subs, chain, nseg) == 0, (n, seam)
 
 
 @pytest.mark.parametrize("sides", [1, 2])
@@ -64,3 +65,11 @@ def test_tile_widths(replay, gated, b_mn):
         for bn in (128, 192, 256):
             c = replay.columns(bn, N, gated, b_mn, 1, 0)
             assert c <= bn and c % 64 == 0 and (c == bn or need <= c < need + 128)
+
+
+def test_fp32_chains_stay_short(replay):
+    """A reduction of any length: no accumulator of an fp32 product sums more than 12 k-blocks (there were seven segments
+    at most, as long as it took)."""
+    for n in [*range(1, 400), 1024, 2048, 4000]:
+        assert replay.longest_chain(n, 1, 12) <= 12, n
+        assert replay.longest_chain(n, 2, 14) <= 14, n

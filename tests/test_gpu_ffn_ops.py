@@ -505,6 +505,20 @@ def test_fp32_products_are_fp32():
         assert ((y.double() - want).norm() / want.norm()).item() < 1e-6
 
 
+@pytest.mark.parametrize("M,N,K", [(1100, 2000, 16384), (1100, 2000, 5400), (300, 200, 40000), (64, 64, 100000)])
+def test_fp32_products_of_long_reductions(M, N, K):
+    """The error relative to the result does not grow with the reduction: its accumulators' chains are no longer than
+    those of K = 1500 (errors of independent chains add up as the chains do), and the fp32 additions of the K / 768
+    chains are off by 2^-24 each, 4e-8 sqrt(K / 768) of the result together: half of the bound at K = 100000."""
+    n = T.normals(M + K)
+    x, w, y = n(M, K), n(N, K, std=K ** -0.5), torch.empty(M, N, device="cuda")
+    W.op_linear_act(W.FP32, x, w, None, y, M, N, K)
+    want = x.double() @ w.double().t()
+    assert ((y.double() - want).norm() / want.norm()).item() < 1e-6
+    _, _, y64, ey = T.linear64(x, w, None, None, "none", FP)
+    T.within(y, y64, ey)
+
+
 @pytest.mark.parametrize("t", [BF, FP])
 def test_linear_special_values(t):
     """A row with a NaN or an infinity spoils itself only; infinite pre-activations have their limits."""
