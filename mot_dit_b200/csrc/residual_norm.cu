@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(NV == 24 ? 384 : 512) res_norm_grad_kernel(con
     if (KEEP) done();
     row_sum<6>(v, t, tpr, ry, R, sh, phase, n);
     const float r = rsqrtf(v[0] * inv + kEps);
-    const float c = r * r * r * (v[1] * inv);
+    const float c = r * (r * (r * (v[1] * inv)));  // (r^3 alone leaves fp32's range at rows of 1e12, and r_y^2 / D at 1e17)
     const float rp = f.post ? rsqrtf(v[2] * inv + kEps) : 1.f;
-    const float cy = f.post ? rp * rp * inv * (v[3] + r * v[4] - c * v[5]) : 0.f;
+    const float cy = f.post ? rp * (rp * (inv * (v[3] + r * v[4] - c * v[5]))) : 0.f;
     const f2 r2 = bits2(r, r), nc2 = bits2(-c, -c), rp2 = bits2(rp, rp), ncy2 = bits2(-cy, -cy), al2 = bits2(f.alpha, f.alpha);
 #pragma unroll
     for (int k = 0; k < NV / 8; ++k) {

@@ -325,6 +325,36 @@ def test_residual_norm_backward(M, per, D, r, t, post, gate, mod, gain, alpha):
 
 
 @pytest.mark.parametrize("r,t", [(FP, BF), (BF, BF), (FP, FP)])
+@pytest.mark.parametrize("scale", [1e-8, 1.0, 1e13, 1e15, 1e17])
+@pytest.mark.parametrize("D", [96, 4100])
+def test_residual_norm_backward_of_any_magnitude(D, scale, r, t):
+    """A stream of large or small rows, and no gradient from it: dx = r (dn - n mean(dn n)) alone."""
+    M = 33
+    n = T.normals(D)
+    s, y, dh, gain = n(M, D, std=scale, dtype=r), n(M, D, dtype=t), n(M, D, dtype=t), n(D, mean=1.0)
+    (dx, ok1), (dy, ok2) = T.guarded((M, D), r), T.guarded((M, D), t)
+    W.op_residual_norm_backward(CODE[t], s, y, None, dh, dx, dy, M, D, gain=gain, res_dtype=CODE[r])
+    S, dn = s.double(), dh.double() * gain.double()
+    rs = 1 / ((S * S).mean(1, keepdim=True) + T.EPS).sqrt()
+    want = rs * dn - S * rs ** 3 * (dn * S).mean(1, keepdim=True)
+    # the statistic and the mean: D additions and a few roundings of either term
+    e = (D + 32) * 2.0 ** -23 * (rs * dn.abs() + S.abs() * rs ** 3 * (dn * S).abs().mean(1, keepdim=True))
+    T.within(dx, want, e + T.H[r] * (want.abs() + e))
+    T.within(dy, want, e + T.H[t] * (want.abs() + e))
+    ok1(), ok2()
+    # the same of the post-norm: dy = r_y (dv - q mean(dv q)), q = y r_y, from a stream of ordinary size
+    s, y, ds = n(M, D, dtype=r), n(M, D, std=scale, dtype=t), n(M, D, dtype=r)
+    W.op_residual_norm_backward(CODE[t], s, y, ds, dh, dx, dy, M, D, post_norm=True, gain=gain, res_dtype=CODE[r])
+    S, Y = s.double(), y.double()
+    rs, ry = (1 / ((v * v).mean(1, keepdim=True) + T.EPS).sqrt() for v in (S, Y))
+    dv = ds.double() + rs * dn - S * rs ** 3 * (dn * S).mean(1, keepdim=True)
+    want = ry * (dv - Y * ry ** 2 * (dv * Y).mean(1, keepdim=True))
+    size = ds.double().abs() + rs * dn.abs() + S.abs() * rs ** 3 * (dn * S).abs().mean(1, keepdim=True)
+    e = (D + 32) * 2.0 ** -22 * ry * (size + Y.abs() * ry ** 2 * (size * Y.abs()).mean(1, keepdim=True))
+    T.within(dy, want, e + T.H[t] * (want.abs() + e))
+
+
+@pytest.mark.parametrize("r,t", [(FP, BF), (BF, BF), (FP, FP)])
 @pytest.mark.parametrize("M,per,D", [(19, 7, 4001), (13, 5, 8191), (700, 350, 4001), (1, 0, 7681)])
 def test_residual_norm_wide_odd(M, per, D, r, t):
     """Wide rows without vector accesses, 16 and 24 columns a thread, in every type: both directions."""
