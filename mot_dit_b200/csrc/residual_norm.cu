@@ -27,47 +27,14 @@
 #include "cluster.cuh"
 #include "kernels.h"
 #include "op_epilogue.cuh"
+#include "row_plan.h"
 
 namespace wam {
 namespace {
 
 constexpr float kEps = 1e-6f;
-constexpr int kRowThreads = 224;  // row threads of a block when a row needs fewer (256 with the producer)
-constexpr int kMaxStages = 8;
-constexpr int kRing = 56 * 1024;      // ring of a block (several blocks an SM) ...
-constexpr int kSmem = 224 * 1024; // ... when two stages fit it, else what a block can have
 
 __device__ unsigned g_norm_status;
-
-// Threads that share a row: NV elements each; a power of two below a warp,
-// whole warps above.
-int row_threads(int D, int nv) {
-  const int t = (D + nv - 1) / nv;
-  if (t > 32) return (t + 31) / 32 * 32;
-  int p = 1;
-  while (p < t) p *= 2;
-  return p;
-}
-int rows_at_once(int tpr) { return tpr >= kRowThreads ? 1 : kRowThreads / tpr; }
-int elems(int D) { return D > 7680 ? 24 : D > 3840 ? 16 : 8; }  // (blocks of at most 512, 512, 384 threads)
-
-// The ring's shape: `rows` rows of up to four matrices a stage.
-struct Ring {
-  int stages, stage_bytes;
-  int off[4];  // of each matrix in a stage
-};
-Ring ring_of(int D, int rows, int reserved, std::initializer_list<int> sizes) {
-  Ring r{};
-  int at = 0, i = 0;
-  for (int e : sizes) {
-    r.off[i++] = at;
-    at += (rows * D * e + 15) / 16 * 16 + 16;  // (a span that starts inside a granule takes one more)
-  }
-  r.stage_bytes = (at + 127) / 128 * 128;
-  const int budget = 2 * r.stage_bytes <= kRing ? kRing : kSmem - reserved;
-  r.stages = std::max(1, std::min(kMaxStages, budget / r.stage_bytes));
-  return r;
-}
 
 // Element j of thread t: groups of E consecutive elements, a row's threads
 // side by side (E = 8 where 16-byte accesses may be used, else 1).
@@ -648,21 +615,12 @@ __global__ void __launch_bounds__(1024) res_norm_sum_kernel(const ResNormGrad a,
   }
 }
 
-// Chunks of rows per sample: as many blocks as run at once (two an SM, one of
-// more than 256 threads), each of at least four passes of its row lanes.
-int grad_chunks(int M, int D, int rpg) {
-  const int tpr = row_threads(D, elems(D)), rows = rows_at_once(tpr), blocks = tpr * rows <= 224 ? 296 : 148;
-  const int groups = (M + rpg - 1) / rpg;
-  const int most = (std::min(rpg, M) + 4 * rows - 1) / (4 * rows);
-  return std::max(1, std::min(most, (blocks + groups - 1) / groups));
-}
-
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const int tpr = row_threads(a.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
-  const int coef = NV == 8 ? 0 : 3 * ((a.D + 7) / 8 * 8) * 4;
+  const int coef = coef_bytes(a.D, 3);
   const Ring ring = ring_of(a.D, R, coef, {(int)sizeof(RT), (int)sizeof(CT)});
   const int smem = ring.stages * ring.stage_bytes + coef;
   auto* kernel = NV == 8 && threads <= 256 ? res_norm_kernel<E, NV, NV == 8, RT, CT> : res_norm_kernel<E, NV, false, RT, CT>;
@@ -672,16 +630,15 @@ cudaError_t run_fwd(const ResNorm& a, cudaStream_t s) {
   const int sms = current_sms();
   if (!sms) return cudaErrorNoDevice;
   // as many blocks as run at once: by registers (see the launch bounds) and by shared memory
-  const int per = std::min(threads > 256 ? 1 : NV == 8 ? (E == 8 ? 3 : 2) : 1, 227 * 1024 / (smem + 3 * 1024));
+  const int per = std::min(threads > 256 ? 1 : NV == 8 ? (E == 8 ? 3 : 2) : 1, kSmemOfSm / (smem + kStaticSmem));
   const int grid = std::max(1, std::min((a.M + R - 1) / R, sms * std::max(1, per)));
   return launch_k(kernel, dim3(grid), dim3(threads), smem, s, a, ring, tpr, R);
 }
 template <int E, int NV, typename RT, typename CT>
 cudaError_t run_bwd(const ResNormGrad& a, int chunks, int groups, cudaStream_t s) {
   const int tpr = row_threads(a.f.D, NV), R = rows_at_once(tpr), threads = tpr * R + 32;
-  const int coef = NV == 8 ? 0 : 2 * ((a.f.D + 7) / 8 * 8) * 4;
-  const Ring ring = ring_of(a.f.D, R, coef, {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
-  const int smem = std::max(ring.stages * ring.stage_bytes + coef, R > 1 ? R * 3 * tpr * NV * 4 : 0);
+  const Ring ring = ring_of(a.f.D, R, coef_bytes(a.f.D, 2), {(int)sizeof(RT), (int)sizeof(CT), (int)sizeof(CT), (int)sizeof(RT)});
+  const int smem = grad_smem(ring, a.f.D);
   auto* kernel = res_norm_grad_kernel<E, NV, RT, CT>;
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = allow_smem(kernel, kSmem, done);

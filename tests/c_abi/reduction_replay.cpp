@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "op_reduction.h"
+#include "row_plan.h"
 
 using namespace wam;
 
@@ -64,3 +65,11 @@ extern "C" int replay_backward(int f32, int M, int N, int K, int sides) {
 extern "C" int pieces_dx(int f32, int M, int N, int K, int sides) { return pieces_for(f32, M, N, K, sides).dx; }
 extern "C" int columns(int bn, int N, int gated, int b_mn, int pair, int f32) { return tile_columns(bn, N, gated, b_mn, pair, f32); }
 extern "C" int longest_chain(int n, int subs, int chain) { return std::min(n, segments_of(0, n, n, subs, chain).per * subs); }
+// A backward norm block of D columns (element sizes of the stream and of the rest): bytes, and the stages of its ring.
+extern "C" int grad_block(int D, int stream, int rest, int* stages, int* planned) {
+  const int R = rows_at_once(row_threads(D, elems(D)));
+  const Ring r = ring_of(D, R, coef_bytes(D, 2), {stream, rest, rest, stream});
+  *stages = r.stages;
+  *planned = grad_blocks_per_sm(D);
+  return grad_smem(r, D) + kStaticSmem;
+}

@@ -73,3 +73,13 @@ def test_fp32_chains_stay_short(replay):
     for n in [*range(1, 400), 1024, 2048, 4000]:
         assert replay.longest_chain(n, 1, 12) <= 12, n
         assert replay.longest_chain(n, 2, 14) <= 14, n
+
+
+@pytest.mark.parametrize("stream,rest", [(4, 2), (2, 2), (4, 4)])
+def test_norm_blocks_fit_as_planned(replay, stream, rest):
+    """The chunks of the backward norm count on as many blocks an SM as its shared memory holds (at 32, 64, 128, 256 and
+    1792 columns of fp32 one ran where two were planned)."""
+    stages, planned = C.c_int(), C.c_int()
+    for D in range(1, 8193):
+        need = replay.grad_block(D, stream, rest, C.byref(stages), C.byref(planned))
+        assert stages.value >= 1 and need * planned.value <= 227 * 1024, (D, need, planned.value)
