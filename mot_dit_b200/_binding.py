@@ -448,6 +448,14 @@ class _Args:
         return x.data_ptr(), x.numel() * x.element_size()
 
 
+def _int32(where: str, bits: int, *signed: int):
+    """bits: the bitwise or of a call's types, sizes and kinds, none of them
+    negative in a valid call; signed: integers that may be.  The library takes 32
+    bits of each, and ctypes would drop the others."""
+    if bits >> 31 or any(not -1 << 31 <= v < 1 << 31 for v in signed):
+        raise WamError(1, where, "a size, type or activation that is negative or not below 2^31")
+
+
 def _done(st: int, where: str):
     if st:
         raise WamError(st, where)
@@ -462,6 +470,7 @@ def op_linear_act(dtype, x, w, bias, y, M, N, K, act=0, residual=None, z=None, o
     """y = act(z) + residual, z = x w^T + bias (wam_op_linear_act).  act: an index
     of ACTS; residual may be y; z: where to save the pre-activation, or None."""
     where, out = "wam_op_linear_act", dtype if out_dtype is None else out_dtype
+    _int32(where, dtype | out | M | N | K | act)
     a = _Args(where)
     _done(lib().wam_op_linear_act(dtype, out, a("x", x, dtype, M * K), a("w", w, dtype, N * K), a("bias", bias, FP32, N),
                                   a("residual", residual, out, M * N), a("y", y, out, M * N), a("z", z, dtype, M * N),
@@ -470,15 +479,16 @@ def op_linear_act(dtype, x, w, bias, y, M, N, K, act=0, residual=None, z=None, o
 
 def op_linear_act_workspace(dtype, M, N, K, act=0, dy_dtype=None) -> int:
     """Workspace bytes of op_linear_act_backward."""
-    n = C.c_size_t(0)
-    _done(lib().wam_op_linear_act_workspace(dtype, M, N, K, act, dtype if dy_dtype is None else dy_dtype, C.byref(n)),
-          "wam_op_linear_act_workspace")
+    where, o, n = "wam_op_linear_act_workspace", dtype if dy_dtype is None else dy_dtype, C.c_size_t(0)
+    _int32(where, dtype | o | M | N | K | act)
+    _done(lib().wam_op_linear_act_workspace(dtype, M, N, K, act, o, C.byref(n)), where)
     return n.value
 
 
 def op_linear_act_backward(dtype, x, w, z, dy, dx, dw, db, M, N, K, act=0, dy_dtype=None, workspace=None, stream=None):
     """Gradients of op_linear_act (each of dx, dw, db may be None)."""
     where, o = "wam_op_linear_act_backward", dtype if dy_dtype is None else dy_dtype
+    _int32(where, dtype | o | M | N | K | act)
     a = _Args(where)
     ws, n = a.workspace(workspace, 1 << 62)
     _done(lib().wam_op_linear_act_backward(dtype, o, a("x", x, dtype, M * K), a("w", w, dtype, N * K),
@@ -491,6 +501,7 @@ def op_gated(dtype, x, wg, wu, a, M, F, K, act=ACTS.index("silu"), bias_g=None, 
     """a = act(x wg^T + bias_g) (x wu^T + bias_u) (wam_op_gated); g and u: where
     to save the two pre-activations, or None."""
     where = "wam_op_gated"
+    _int32(where, dtype | M | F | K | act)
     c = _Args(where)
     _done(lib().wam_op_gated(dtype, c("x", x, dtype, M * K), c("wg", wg, dtype, F * K), c("wu", wu, dtype, F * K),
                              c("bias_g", bias_g, FP32, F), c("bias_u", bias_u, FP32, F), c("a", a, dtype, M * F),
@@ -499,8 +510,9 @@ def op_gated(dtype, x, wg, wu, a, M, F, K, act=ACTS.index("silu"), bias_g=None, 
 
 def op_gated_workspace(dtype, M, F, K) -> int:
     """Workspace bytes of op_gated_backward."""
-    n = C.c_size_t(0)
-    _done(lib().wam_op_gated_workspace(dtype, M, F, K, C.byref(n)), "wam_op_gated_workspace")
+    where, n = "wam_op_gated_workspace", C.c_size_t(0)
+    _int32(where, dtype | M | F | K)
+    _done(lib().wam_op_gated_workspace(dtype, M, F, K, C.byref(n)), where)
     return n.value
 
 
@@ -508,6 +520,7 @@ def op_gated_backward(dtype, x, wg, wu, g, u, da, dx, dwg, dwu, M, F, K, act=ACT
                       dbias_u=None, workspace=None, stream=None):
     """Gradients of op_gated (dx, the weights' pair and the biases' pair may each be None)."""
     where = "wam_op_gated_backward"
+    _int32(where, dtype | M | F | K | act)
     c = _Args(where)
     ws, n = c.workspace(workspace, 1 << 62)
     _done(lib().wam_op_gated_backward(dtype, c("x", x, dtype, M * K), c("wg", wg, dtype, F * K), c("wu", wu, dtype, F * K),
@@ -526,6 +539,7 @@ def op_residual_norm(dtype, x, y, s, h, M, D, post_norm=False, post_gain=None, g
     """s = alpha x + gate p, p = y or post_gain rms(y); h = rms(s) gain (1 + scale)
     + shift (wam_op_residual_norm).  s may be x, h may be y."""
     where, ld = "wam_op_residual_norm", ld_mod or D
+    _int32(where, dtype | res_dtype | M | D | rows_per_group, ld)
     c, G = _Args(where), _groups(M, rows_per_group)
     _done(lib().wam_op_residual_norm(dtype, res_dtype, c("x", x, res_dtype, M * D), c("y", y, dtype, M * D),
                                      c("s", s, res_dtype, M * D), c("h", h, dtype, M * D), M, D, alpha, int(post_norm),
@@ -536,8 +550,9 @@ def op_residual_norm(dtype, x, y, s, h, M, D, post_norm=False, post_gain=None, g
 
 def op_residual_norm_workspace(M, D, rows_per_group=0) -> int:
     """Workspace bytes of op_residual_norm_backward."""
-    n = C.c_size_t(0)
-    _done(lib().wam_op_residual_norm_workspace(M, D, rows_per_group, C.byref(n)), "wam_op_residual_norm_workspace")
+    where, n = "wam_op_residual_norm_workspace", C.c_size_t(0)
+    _int32(where, M | D | rows_per_group)
+    _done(lib().wam_op_residual_norm_workspace(M, D, rows_per_group, C.byref(n)), where)
     return n.value
 
 
@@ -548,6 +563,7 @@ def op_residual_norm_backward(dtype, s, y, ds, dh, dx, dy, M, D, post_norm=False
     None (zero), every parameter gradient too (not computed).  dx may be ds or
     s, dy may be dh or y."""
     where, ld = "wam_op_residual_norm_backward", ld_mod or D
+    _int32(where, dtype | res_dtype | M | D | rows_per_group, ld)
     c, G = _Args(where), _groups(M, rows_per_group)
     ws, nb = c.workspace(workspace, 1 << 62)
     _done(lib().wam_op_residual_norm_backward(

@@ -149,3 +149,26 @@ def test_binding_checks_tensors():
         W.op_residual_norm(W.BF16, P, 2 * P, 3 * P, 4 * P, M, D, gate=torch.zeros(2, D), rows_per_group=4)
     with pytest.raises(W.WamError):
         W.op_gated_backward(W.BF16, P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, 7 * P, 8 * P, 9 * P, M, N, K, workspace=torch.zeros(1 << 20))
+
+
+BIG = 1 << 32
+
+
+@pytest.mark.parametrize("call", [
+    lambda: W.op_linear_act_workspace(W.BF16, BIG + M, N, K), lambda: W.op_linear_act_workspace(W.BF16, M, N, K, act=BIG),
+    lambda: W.op_gated_workspace(W.BF16, M, BIG + N, K), lambda: W.op_gated_workspace(BIG + W.BF16, M, N, K),
+    lambda: W.op_residual_norm_workspace(BIG + M, D), lambda: W.op_residual_norm_workspace(M, D, BIG + 1),
+    lambda: W.op_linear_act(W.BF16, P, 2 * P, 3 * P, 4 * P, BIG, N, K), lambda: W.op_linear_act(W.BF16, P, 2 * P, 3 * P, 4 * P, M, N, -K),
+    lambda: W.op_linear_act_backward(W.BF16, P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, 7 * P, M, BIG + N, K, workspace=8 * P),
+    lambda: W.op_gated(W.BF16, P, 2 * P, 3 * P, 4 * P, BIG, N, K),
+    lambda: W.op_gated_backward(W.BF16, P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, 7 * P, 8 * P, 9 * P, M, N, BIG + K, workspace=10 * P),
+    lambda: W.op_residual_norm(W.BF16, P, 2 * P, 3 * P, 4 * P, BIG, D),
+    lambda: W.op_residual_norm(W.BF16, P, 2 * P, 3 * P, 4 * P, M, D, gate=5 * P, rows_per_group=4, ld_mod=BIG + D),
+    lambda: W.op_residual_norm_backward(W.BF16, P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, BIG, D),
+])
+def test_binding_refuses_what_32_bits_cannot_hold(call):
+    """ctypes would pass a size's low 32 bits on (a workspace for 16 rows where 2^32 + 16 were asked for)."""
+    with pytest.raises(W.WamError) as e:
+        call()
+    assert e.value.status == 1
+    assert W.op_residual_norm_workspace(M, D, 1) == M * 3 * D * 4  # (and ordinary sizes pass)
