@@ -1,6 +1,7 @@
 // C ABI of the feed-forward and residual-norm operators (include/wam.h):
 // argument checks, workspace layout and the launches of each direction.
 #include <initializer_list>
+#include <utility>
 
 #include "kernels.h"
 #include "op_reduction.h"
@@ -14,7 +15,7 @@ constexpr int kMaxDim = 1 << 24;  // rows, features (tile and chunk counts stay 
 
 wam_status status_of(cudaError_t e) {
   if (e == cudaSuccess) return WAM_OK;
-  (void)cudaGetLastError();  // a refused launch is reported here, not by the caller's next call
+  (void)cudaGetLastError();  // what failed is reported here, not by the caller's next call
   if (e == cudaErrorMemoryAllocation) return WAM_ERR_OOM;
   return WAM_ERR_CUDA;
 }
@@ -24,6 +25,15 @@ size_t esize(int dtype) { return dtype == WAM_FP32 ? 4 : 2; }
 bool is_type(int t) { return t == WAM_FP32 || t == WAM_BF16; }
 bool is_dim(int n) { return n >= 1 && n <= kMaxDim; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Zeroes the outputs of a call without rows.
+wam_status zero(std::initializer_list<std::pair<void*, size_t>> outs, cudaStream_t s) {
+  for (const auto& o : outs) {
+    const cudaError_t e = o.first ? cudaMemsetAsync(o.first, 0, o.second, s) : cudaSuccess;
+    if (e != cudaSuccess) return status_of(e);
+  }
+  return WAM_OK;
+}
 
 // A buffer of a call; an empty or null one overlaps nothing.
 struct Span {
@@ -118,7 +128,9 @@ extern "C" {
 
 wam_status wam_ops_check_status(void) {
   unsigned gemm = 0, norm = 0;
-  if (op_gemm_status(&gemm) != cudaSuccess || res_norm_status(&norm) != cudaSuccess) return WAM_ERR_CUDA;
+  cudaError_t e = op_gemm_status(&gemm);
+  if (e == cudaSuccess) e = res_norm_status(&norm);
+  if (e != cudaSuccess) return status_of(e);
   return gemm | norm ? WAM_ERR_TIMEOUT : WAM_OK;
 }
 
@@ -169,11 +181,7 @@ wam_status wam_op_linear_act_backward(int dtype, int dy_dtype, const void* x, co
   cudaStream_t s = (cudaStream_t)stream;
   const size_t e = esize(dtype), o = esize(dy_dtype);
   if ((!dx && !dw && !db) || !aligned(dx, e) || !aligned(dw, e) || !aligned(db, 4)) return WAM_ERR_INVALID_ARG;
-  if (M == 0) {  // no rows: the sums over them are zero
-    if (dw && cudaMemsetAsync(dw, 0, (size_t)N * K * e, s) != cudaSuccess) return WAM_ERR_CUDA;
-    if (db && cudaMemsetAsync(db, 0, (size_t)N * 4, s) != cudaSuccess) return WAM_ERR_CUDA;
-    return WAM_OK;
-  }
+  if (M == 0) return zero({{dw, (size_t)N * K * e}, {db, (size_t)N * 4}}, s);  // no rows: the sums over them are zero
   if ((dw && !x) || (dx && !w) || !dy || (act != kActNone && !z) || !aligned(x, e) || !aligned(w, e) || !aligned(z, e) ||
       !aligned(dy, o) || nbytes < need || (need && (!workspace || !aligned(workspace, 256))))
     return WAM_ERR_INVALID_ARG;
@@ -301,14 +309,7 @@ wam_status wam_op_gated_backward(int dtype, const void* x, const void* wg, const
       !aligned(dwu, e) || !aligned(dbias_g, 4) || !aligned(dbias_u, 4))
     return WAM_ERR_INVALID_ARG;
   const size_t mf = (size_t)M * F, mk = (size_t)M * K, fk = (size_t)F * K;
-  if (M == 0) {
-    if (dwg && (cudaMemsetAsync(dwg, 0, fk * e, s) != cudaSuccess || cudaMemsetAsync(dwu, 0, fk * e, s) != cudaSuccess))
-      return WAM_ERR_CUDA;
-    if (dbias_g && (cudaMemsetAsync(dbias_g, 0, (size_t)F * 4, s) != cudaSuccess ||
-                    cudaMemsetAsync(dbias_u, 0, (size_t)F * 4, s) != cudaSuccess))
-      return WAM_ERR_CUDA;
-    return WAM_OK;
-  }
+  if (M == 0) return zero({{dwg, fk * e}, {dwu, fk * e}, {dbias_g, (size_t)F * 4}, {dbias_u, (size_t)F * 4}}, s);
   if ((dwg && !x) || (dx && (!wg || !wu)) || !g || !u || !da || !aligned(x, e) || !aligned(wg, e) || !aligned(wu, e) ||
       !aligned(g, e) || !aligned(u, e) || !aligned(da, e) || nbytes < need || !workspace || !aligned(workspace, 256))
     return WAM_ERR_INVALID_ARG;
@@ -438,12 +439,8 @@ wam_status wam_op_residual_norm_backward(int dtype, int res_dtype, const void* s
     return WAM_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const size_t vec = (size_t)D * 4;
-  if (M == 0) {  // no rows, no samples: the vectors' gradients are zero, the tables' empty
-    if ((dpost_gain && cudaMemsetAsync(dpost_gain, 0, vec, st) != cudaSuccess) ||
-        (dgain && cudaMemsetAsync(dgain, 0, vec, st) != cudaSuccess))
-      return WAM_ERR_CUDA;
-    return WAM_OK;
-  }
+  // no rows, no samples: the vectors' gradients are zero, the tables' empty
+  if (M == 0) return zero({{dpost_gain, vec}, {dgain, vec}}, st);
   const int rpg = rows_per_group == 0 || rows_per_group > M ? M : rows_per_group;
   const int groups = (M + rpg - 1) / rpg;
   const size_t e = esize(dtype), r = esize(res_dtype), n = (size_t)M * D;

@@ -523,6 +523,41 @@ print("captured first")
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
+def test_a_failed_call_spoils_no_later_one():
+    """A status check inside a capture is refused (it would synchronise), and so is a call on a stream whose capture it
+    ended; neither leaves an error for the calls after them."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import mot_dit_b200 as W
+x, w, y = torch.randn(64, 256, device="cuda"), torch.randn(128, 256, device="cuda"), torch.empty(64, 128, device="cuda")
+db = torch.ones(8, device="cuda")
+torch.cuda.synchronize()
+st = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.stream(st):
+    g.capture_begin()
+    for call in (W.ops_check_status, lambda: W.op_linear_act_backward(W.FP32, None, None, None, None, None, None, db, 0, 8, 256, stream=st)):
+        try:
+            call()
+            raise SystemExit("not refused")
+        except W.WamError as e:
+            assert e.status == 4, e
+    try:
+        g.capture_end()
+    except RuntimeError:
+        pass
+W.op_linear(W.FP32, x, w, torch.zeros(128, device="cuda"), y, 64, 128, 256)
+W.ops_check_status()
+want = x.double() @ w.double().t()
+assert ((y.double() - want).norm() / want.norm()).item() < 1e-5
+print("later call ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "later call ok" in r.stdout, r.stdout + r.stderr[-2000:]
+
+
 def test_fp32_products_are_fp32():
     """Three parts an operand: the sums are as near as an fp32 matrix product's, at any scale of the operands."""
     M, N, K = 200, 300, 1500
