@@ -32,9 +32,9 @@
 //    them (the epilogue's), and six part products are summed.
 //
 // Bound by the tensor pipe and the power cap where tiles are many (8448 x 6144 x
-// 1536 gated: pipe busy 79% of the cycles at 1.55 GHz, 1.39 PFLOP/s; 8448 x
-// 4096 x 1536 gated backward 1.42 PFLOP/s), by start, tail and whole waves where
-// they are few (1088 x 1536 x 6144: 31.6 us, 144 tiles in one wave).
+// 1536 gated: pipe busy 76% of the cycles at 1.69 GHz, 1.55 PFLOP/s; 4224 x
+// 4096 x 1536 gated backward 1.45 PFLOP/s), by start, tail and whole waves where
+// they are few (1088 x 1536 x 6144: 26.6 us in a graph, 144 tiles in one wave).
 //
 // Warp roles: warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warps
 // 2..9 epilogue (warp w reads TMEM lanes 32 (w % 4) ..), kManual: warps 10..13
@@ -329,10 +329,12 @@ __device__ __forceinline__ bool epi_any(bool p) {
 }
 
 // ---- fp32 operands as bf16 parts: x = hi + mid + lo, each the nearest bf16 of
-// what the ones before leave, exact for normal numbers (3 x 8 bits).  Six of
-// the nine products are taken; the other three are below 2^-26 of the exact
-// one.  What rounds to an infinite hi has no other parts (an infinity times
-// a zero part still makes NaN of an infinite operand's row or column).
+// what the ones before leave, exact from 2^-110 in magnitude (3 x 8 bits; below,
+// the last bits of lo would be under bf16's smallest).  Six of the nine products are
+// taken; the other three together reach 2^-24 of the exact one (mid is up to
+// 2^-8 of the operand, lo 2^-17).  What rounds to an infinite hi has no other
+// parts (an infinity times a zero part still makes NaN of an infinite
+// operand's row or column).
 struct Feed {
   int it = 0, st = 0;
   uint32_t phase = 0;
@@ -1114,9 +1116,9 @@ Plan choose(const OpProduct* p, int n, int mode, const Device& d) {
     if (c < bc) bc = c, best = pl;
   };
   // Widths between the powers of two fill the SMs more evenly (1088 x 1536: 144
-  // tiles of 96 columns, 31.6 us; 108 of 128, 33.8 us).  A reduction-outermost
-  // operand takes a load per 64 columns, and they lose there (2049 x 4111 x 1544
-  // backward: 192 wide 111 us, pairs 83 us).
+  // tiles of 96 columns, 26.6 us; 108 of 128, 27.9 us; both in a graph).  A
+  // reduction-outermost operand takes a load per 64 columns, and they lose there
+  // (2049 x 4111 x 1544 backward: 192 wide 103 us, 256 wide 94, pairs 77 us).
   const bool narrow = n == 1 && !p[0].gated && !p[0].b_mn;
   for (int bn = mode == kF32 ? 128 : 256; bn >= 64; bn -= 32) {  // (fp32: six parts of a wider tile leave no second stage)
     if ((bn & (bn - 1)) && (!narrow || mode == kF32)) continue;

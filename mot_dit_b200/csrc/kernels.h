@@ -399,7 +399,8 @@ cudaError_t launch_tacd_targets(const float* a_t, const float* a0_teacher, const
                                 const float* f_ema, float t, float lambda, int B, int per_sample, float* u_ta,
                                 float* v_student, float* u_cd, float* losses, cudaStream_t s);
 
-// ---- feed-forward products, both directions (gemm_ops.cu, ffn_ops.cu) ------
+// ---- feed-forward products, both directions (gemm_ops.cu, skinny_ops.cu,
+// act_grad.cu) and the residual norm (residual_norm.cu) -----------------------
 enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGeluTanh = 3, kActGeluErf = 4, kActSigmoid = 5, kActKinds = 6 };
 
 // Epilogue of one product: out = act(acc + bias) + res (res: out's type, may

@@ -1,6 +1,7 @@
 // Activations with their derivatives, and the fused epilogue of the
 // feed-forward products: bias, activation, gate product, residual and the
-// saved pre-activations.  Shared by the tensor-core and the fp32 kernels.
+// saved pre-activations.  Shared by the products of many rows and of few, and by
+// the activation gradients.
 #pragma once
 
 #include "common.cuh"
@@ -199,35 +200,6 @@ __device__ __forceinline__ void store_any(void* p, bool f32, size_t i, const flo
     store_to<E>(reinterpret_cast<float*>(p) + i, v);
   else
     store_to<E>(reinterpret_cast<__nv_bfloat16*>(p) + i, v);
-}
-// n elements' groups of E at p + at(i), all requested before the first is converted.
-template <int E, int N, typename At>
-__device__ __forceinline__ void load_batch(const void* p, bool f32, At at, float (&v)[N][E]) {
-  if (f32) {
-    Raw<float, E> r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const long long o = at(i);
-      if (o >= 0)
-        r[i].load(reinterpret_cast<const float*>(p) + o);
-      else
-        r[i].zero();
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i].get(v[i]);
-  } else {
-    Raw<__nv_bfloat16, E> r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const long long o = at(i);
-      if (o >= 0)
-        r[i].load(reinterpret_cast<const __nv_bfloat16*>(p) + o);
-      else
-        r[i].zero();
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i].get(v[i]);
-  }
 }
 
 // Eight elements [col, col + 8) of a row, zero outside the matrix, from any

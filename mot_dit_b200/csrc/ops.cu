@@ -11,7 +11,7 @@ using namespace wam;
 
 namespace {
 
-constexpr int kMaxDim = 1 << 24;  // rows, features (tile and chunk counts stay within 32 bits)
+constexpr int kMaxDim = 1 << 24;  // rows, features (the tiles and chunks of what fits a device stay within 32 bits)
 
 wam_status status_of(cudaError_t e) {
   if (e == cudaSuccess) return WAM_OK;
