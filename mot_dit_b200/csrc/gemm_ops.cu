@@ -721,9 +721,10 @@ __global__ void __launch_bounds__(MODE == kManual ? kThreads + kLoaders : kThrea
       const int mw = m0 + quad * 32;
       auto ready = [&] {  // the present buffer is complete (one decision for all warps)
         const bool ok = mbar_wait(&accf[buf], bphase, status, kStatusTimeoutAccum, abort_flag);
-        tc_fence_after();
         const bool stop = epi_any(!ok || *abort_flag);
         if (stop) *abort_flag = 1;
+        // (behind the barrier too: a gated tile of 64 columns has its u from sums that the quarter's other warp wrote)
+        tc_fence_after();
         return !stop;
       };
       auto drained = [&] {  // this warp's reads of the accumulator are done

@@ -584,6 +584,40 @@ def test_fp32_products_of_long_reductions(M, N, K):
     T.within(y, y64, ey)
 
 
+@pytest.mark.parametrize("M,F,K", [(1100, 1000, 6000), (2100, 20, 5500), (300, 3000, 12000)])
+def test_gated_fp32_of_long_reductions(M, F, K):
+    """A gated layer's two halves through several rounds, in tiles of either width."""
+    n = T.normals(M + F)
+    x, wg, wu = n(M, K), n(F, K, std=K ** -0.5), n(F, K, std=K ** -0.5)
+    (a, ok1), (g, ok2), (u, ok3) = (T.guarded((M, F), FP) for _ in range(3))
+    W.op_gated(W.FP32, x, wg, wu, a, M, F, K, g=g, u=u)
+    (a64, ea), (g64, eg), (u64, eu) = T.gated64(x, wg, wu, None, None, "silu")
+    T.within(a, a64, ea), T.within(g, g64, eg), T.within(u, u64, eu)
+    for got, want in ((g, g64), (u, u64)):
+        assert ((got.double() - want).norm() / want.norm()).item() < 1e-6
+    ok1(), ok2(), ok3()
+    a2 = torch.empty_like(a)
+    W.op_gated(W.FP32, x, wg, wu, a2, M, F, K)
+    assert torch.equal(a, a2)
+
+
+@pytest.mark.parametrize("M,F,K", [(1000, 8127, 1100), (64, 20000, 700), (20000, 300, 200)])
+def test_gated_backward_fp32_of_long_reductions(M, F, K):
+    """Rounds of a reduction over two operand pairs, whole and in pieces, and of the weights' over many rows."""
+    n = T.normals(M + F)
+    x, wg, wu = n(M, K), n(F, K, std=K ** -0.5), n(F, K, std=K ** -0.5)
+    g, u, da = n(M, F, std=1.5), n(M, F), n(M, F)
+    outs = [T.guarded(s, FP) for s in ((M, K), (F, K), (F, K), (F,), (F,))]
+    W.op_gated_backward(W.FP32, x, wg, wu, g, u, da, *(o[0] for o in outs[:3]), M, F, K, dbias_g=outs[3][0], dbias_u=outs[4][0],
+                        workspace=_ws(W.op_gated_workspace(W.FP32, M, F, K)))
+    dx, [(dwg, dbg), (dwu, dbu)] = T.gated_grad64(x, wg, wu, g, u, da, "silu")
+    for (got, ok), (want, e) in zip(outs, (dx, dwg, dwu, dbg, dbu)):
+        T.within(got, want, e)
+        ok()
+    for (got, _), (want, _) in zip(outs[:3], (dx, dwg, dwu)):
+        assert ((got.double() - want).norm() / want.norm()).item() < 1.5e-6  # (1e-6 as above, and dg's own roundings)
+
+
 @pytest.mark.parametrize("t", [BF, FP])
 def test_linear_special_values(t):
     """A row with a NaN or an infinity spoils itself only; infinite pre-activations have their limits."""
